@@ -370,6 +370,184 @@ ZHA_API zha_status zha_topp_select(const float *scores, const int32_t *counts, i
                            void *stream);
 
 
+/* ---------------------------------------------------------------------------
+ * Paged caches and rotary positions (no counterpart on the method's pages:
+ * what a serving loop needs around the exact attention of one layer).
+ *
+ * A paged cache keeps the keys and values of many sequences in one pool of
+ * fixed-size pages. Row b of the block table lists the pages of sequence b in
+ * order: its token t lives in page table[b][t / page_size] at row
+ * t % page_size. A serving step is
+ *   zha_paged_plan   lengths -> new pages, positions and cache slots,
+ *   zha_paged_write  rotated queries; rotated keys and values into their slots,
+ *   zha_paged_decode exact attention of the step's query rows.
+ * The conventions at the top of this file hold (device pointers owned by the
+ * caller, asynchronous on `stream`, argument errors synchronous, device errors
+ * in dev_status). Int32 arrays need their natural alignment only.
+ * ------------------------------------------------------------------------- */
+
+/* Layouts, dtype = cfg->dtype for q, k_new, v_new, out and the pools:
+ *   kpool, vpool [n_pages][n_kv_heads][page_size][head_dim]
+ *   table        [batch][max_pages] int32  page of each page_size tokens
+ *   lens         [batch] int32             tokens in each sequence's cache
+ * Supported: head_dim in {64, 128}; n_q_heads / n_kv_heads <= 16; page_size a
+ * power of two in [1, 1024]; batch <= 4096; n_pages * page_size and
+ * max_pages * page_size <= 2^30; dtype BF16 or F32. */
+typedef struct zha_paged_config {
+    int32_t batch;       /* sequences: rows of the block table */
+    int32_t n_q_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t dtype;       /* ZHA_BF16 or ZHA_F32 */
+    int32_t page_size;   /* tokens per page */
+    int32_t n_pages;     /* pages in the pool */
+    int32_t max_pages;   /* columns of the block table */
+    float scale;         /* s; <= 0 selects 1/sqrt(head_dim) */
+    int32_t window;      /* > 0: a row attends its newest `window` tokens; 0: all */
+    int32_t reserved[2]; /* zero */
+} zha_paged_config;
+
+/* ZHA_OK if the configuration is supported; otherwise why not. */
+ZHA_API zha_status zha_paged_check_config(const zha_paged_config *cfg);
+
+/* Where a step's new tokens go, one entry per row of the step's (padded)
+ * token buffer. Device pointers.
+ *   positions [max_tokens] int32  position of the token in its sequence
+ *   slots     [max_tokens] int32  page * page_size + row of its cache row; -1: none
+ *   seq_ids   [max_tokens] int32  its sequence (row of the block table); -1: none
+ *   cu_new    [batch + 1]  int32  tokens of sequence b: [cu_new[b], cu_new[b+1])
+ * Rows that belong to no token or to a token that was not served have
+ * position 0, slot -1 and sequence -1. */
+typedef struct zha_token_map {
+    int32_t *positions, *slots, *seq_ids, *cu_new;
+    int32_t max_tokens;  /* rows of the token buffer */
+    int32_t reserved;
+} zha_token_map;
+
+/*
+ * zha_paged_plan -- block tables and slot maps of one step, from the requests'
+ * lengths. n_new[b] >= 0: sequence b (lens[b] tokens cached) gets n_new[b]
+ * tokens, which take the next rows of the token buffer; n_new[b] < 0: the
+ * sequence ends, its pages go back and its length becomes 0.
+ * free_pages [n_pages] with *n_free entries in use is a stack: first the pages
+ * of the sequences that end are pushed (by sequence, then by position), then
+ * the pages the others need are popped in the same order; table gets the new
+ * entries, lens_out [batch] the new lengths, *n_free_out the new count.
+ * lens_out may be lens and n_free_out may be n_free. Nothing else of the table
+ * is written. A sequence is served whole or not at all: one that does not fit
+ * the table's width, the token buffer, or (counting every earlier sequence's
+ * need) the free pages keeps its length, its tokens get no slot, and
+ * ZHA_ERR_CAPACITY is set. ZHA_ERR_INVALID_ARG is set, and nothing done for
+ * the sequence, where a length is negative or beyond the table; and for every
+ * sequence where *n_free is out of range or more pages come back than the
+ * stack holds. A page number outside the pool that is met on the way also
+ * sets ZHA_ERR_INVALID_ARG; tokens on it get no slot.
+ * One launch. Uses batch, page_size, n_pages and max_pages of cfg.
+ */
+ZHA_API zha_status zha_paged_plan(const zha_paged_config *cfg, int32_t *table, const int32_t *lens,
+                                  const int32_t *n_new, int32_t *free_pages, const int32_t *n_free,
+                                  int32_t *lens_out, int32_t *n_free_out, const zha_token_map *map,
+                                  int32_t *dev_status, void *stream);
+
+/* Pairing of the rotated coordinates: (i, i + rotary_dim/2) or (2i, 2i + 1). */
+enum { ZHA_ROPE_HALF = 0, ZHA_ROPE_INTERLEAVED = 1 };
+/* scalings of zha_rotary_freqs */
+enum { ZHA_ROPE_PLAIN = 0, ZHA_ROPE_LINEAR = 1, ZHA_ROPE_NTK = 2, ZHA_ROPE_YARN = 3 };
+
+/* A rotary embedding: pair i of a head at position n turns by n * freq[i]
+ * full turns and is scaled by mscale; coordinates from rotary_dim on pass
+ * through. freq is a DEVICE array of rotary_dim / 2 doubles (in turns per
+ * position, so that the angle of a far position is reduced exactly). */
+typedef struct zha_rotary {
+    int32_t rotary_dim;  /* even, 2 .. head_dim */
+    int32_t layout;      /* ZHA_ROPE_HALF or ZHA_ROPE_INTERLEAVED */
+    float mscale;        /* finite */
+    int32_t reserved;    /* zero */
+    const double *freq;
+} zha_rotary;
+
+/*
+ * zha_rotary_freqs -- the table of a rotary embedding; host memory, no device
+ * work. With theta_i = base^(-2i / rotary_dim), freq[i] = f_i / 2 pi where
+ *   ZHA_ROPE_PLAIN   f_i = theta_i
+ *   ZHA_ROPE_LINEAR  f_i = theta_i / factor (position interpolation)
+ *   ZHA_ROPE_NTK     theta_i of the base base * factor^(rd / (rd - 2))
+ *   ZHA_ROPE_YARN    f_i = (1 - g) theta_i / factor + g theta_i, where g rises
+ *                    linearly from 0 at 1 to 1 at 32 turns of pair i over
+ *                    original_len positions; *mscale = 0.1 ln(factor) + 1
+ * and *mscale = 1 but for YaRN. rotary_dim even in [2, 256], base > 1,
+ * factor > 0 (YaRN: factor >= 1, original_len >= 1); otherwise
+ * ZHA_ERR_INVALID_ARG (nothing written).
+ */
+ZHA_API zha_status zha_rotary_freqs(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                    int64_t original_len, double *freq, float *mscale);
+
+/*
+ * zha_rotary_apply -- rotate the queries and keys of n_tokens tokens:
+ *   q [n_tokens][n_q_heads][head_dim], k [n_tokens][n_k_heads][head_dim]
+ * at positions [n_tokens] (any int32). Tokens are q_stride / k_stride elements
+ * apart (0: contiguous; a slice of a packed projection otherwise), likewise
+ * the outputs; strides are multiples of 16 bytes. An output may be its input
+ * (same pointer and stride); other overlaps are not supported. Either of q and
+ * k may be absent (null, with its output). transpose != 0 applies the
+ * transposed map, which is the gradient of the rotation (and, for mscale 1,
+ * its inverse). Sines and cosines come from fp64 angles, products are fp32,
+ * each output is rounded once. dtype ZHA_BF16 or ZHA_F32, head_dim 64 or 128.
+ */
+ZHA_API zha_status zha_rotary_apply(const zha_rotary *rotary, int32_t head_dim, int32_t dtype,
+                                    int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+                                    const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                    const int32_t *positions, void *q_out, int64_t q_out_stride,
+                                    void *k_out, int64_t k_out_stride, int32_t transpose, void *stream);
+
+/*
+ * zha_paged_write -- rotate a step's queries and keys and put its keys and
+ * values into the cache, in one launch. Token i (of n_tokens rows) has its
+ * position in positions[i] and its cache row in slots[i]; a row with a
+ * negative slot is skipped: neither the cache nor q_out is written for it.
+ * A slot beyond the pool is skipped too and sets ZHA_ERR_INVALID_ARG.
+ * rotary may be null (queries and keys are copied; positions may be null
+ * then), q may be null (with q_out). q_out is contiguous and may be q where q
+ * is contiguous; q_stride, k_stride, v_stride as in zha_rotary_apply. Slots
+ * of different tokens are distinct; where two are equal the cache row's
+ * contents are unspecified (some of each).
+ */
+ZHA_API zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary *rotary,
+                                   int32_t n_tokens, const void *q, int64_t q_stride, const void *k_new,
+                                   int64_t k_stride, const void *v_new, int64_t v_stride,
+                                   const int32_t *positions, const int32_t *slots, void *q_out,
+                                   void *kpool, void *vpool, int32_t *dev_status, void *stream);
+
+/* Bytes of scratch zha_paged_decode needs for up to n_rows rows. Zero it once
+ * before its first use: every call leaves its counters at zero again. One
+ * workspace serves one call at a time (calls that can overlap on the GPU, and
+ * graphs that can, need one each). 0 for a bad config or n_rows < 1. */
+ZHA_API size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_rows);
+
+/*
+ * zha_paged_decode -- exact softmax attention of n_rows single query rows
+ * over the paged cache:
+ *   out[r][h] = sum_t softmax_t(s q[r][h].k_t) v_t,
+ *   lse[r][h] = ln sum_t e^{s q[r][h].k_t}   (fp32, optional: null = not written)
+ * q, out [n_rows][n_q_heads][head_dim]; lse [n_rows][n_q_heads]. Row r belongs
+ * to sequence seq_ids[r] (null: sequence r, n_rows <= batch) and attends its
+ * tokens 0 .. positions[r] (null: all lens[seq] of them), the newest
+ * cfg->window of them if that is set. A row with a negative sequence is left
+ * as it is in out and lse. A row without tokens gets zeros and -inf. A length
+ * beyond the table sets ZHA_ERR_CAPACITY, a sequence beyond the batch or a
+ * position outside [0, lens) ZHA_ERR_INVALID_ARG: the row gets zeros and -inf
+ * (beyond the batch: is left). A page number outside the pool sets
+ * ZHA_ERR_INVALID_ARG and its tokens are skipped. Cache rows outside the
+ * attended range are not read into any result, whatever they hold. Softmax
+ * statistics and sums are fp32. The result does not depend on timing (a split
+ * row's parts are joined in a fixed order).
+ */
+ZHA_API zha_status zha_paged_decode(const zha_paged_config *cfg, int32_t n_rows, const void *q,
+                                    const void *kpool, const void *vpool, const int32_t *table,
+                                    const int32_t *lens, const int32_t *seq_ids, const int32_t *positions,
+                                    void *out, float *lse, void *workspace, int32_t *dev_status,
+                                    void *stream);
+
 /* schedules of zha_p_schedule */
 enum { ZHA_P_FIXED = 0, ZHA_P_DEPTH_ROOT = 1 };
 

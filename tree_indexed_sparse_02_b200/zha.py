@@ -22,6 +22,8 @@ ZHA_FLAG_FUSED_ROUTE = 4
 ZHA_P_FIXED, ZHA_P_DEPTH_ROOT = 0, 1
 ZHA_WAIT_ROW_BARRIER, ZHA_WAIT_MBARRIER = 0, 1
 ZHA_SUMMARY_NATIVE, ZHA_SUMMARY_MXFP8 = 0, 1
+ZHA_ROPE_HALF, ZHA_ROPE_INTERLEAVED = 0, 1
+ZHA_ROPE_PLAIN, ZHA_ROPE_LINEAR, ZHA_ROPE_NTK, ZHA_ROPE_YARN = 0, 1, 2, 3
 ZHA_MAX_LEVELS = 8
 STATUS_NAMES = {0: "ZHA_OK", 1: "ZHA_ERR_INVALID_ARG", 2: "ZHA_ERR_UNSUPPORTED",
                 3: "ZHA_ERR_CAPACITY", 4: "ZHA_ERR_CUDA", 5: "ZHA_ERR_TIMEOUT"}
@@ -59,6 +61,27 @@ class LevelView(ctypes.Structure):
                 ("scores", ctypes.c_size_t), ("kept_mask", ctypes.c_size_t), ("count", ctypes.c_size_t)]
 
 
+class PagedConfig(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == ZHA_BF16 else torch.float32
+
+
+class TokenMap(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("seq_ids", ctypes.c_void_p),
+                ("cu_new", ctypes.c_void_p), ("max_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("freq", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libzha.so not built at {LIB_PATH}; run tree_indexed_sparse_02_b200/build.py")
@@ -66,6 +89,8 @@ def _load():
     P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     CP = ctypes.POINTER(Config)
     SP = ctypes.POINTER(Selection)
+    PP, RP, MP = ctypes.POINTER(PagedConfig), ctypes.POINTER(RotaryDesc), ctypes.POINTER(TokenMap)
+    f64 = ctypes.c_double
     sig = {
         "zha_status_string": ([i32], ctypes.c_char_p),
         "zha_check_config": ([CP], i32),
@@ -88,6 +113,13 @@ def _load():
         "zha_topp_select": ([P, P, i32, i64, f32, P, P, P], i32),
         "zha_p_schedule": ([f32, i32, i32, ctypes.POINTER(f32)], i32),
         "zha_wait_expiry_check": ([i32, i64, P, P], i32),
+        "zha_paged_check_config": ([PP], i32),
+        "zha_paged_plan": ([PP, P, P, P, P, P, P, P, MP, P, P], i32),
+        "zha_rotary_freqs": ([i32, f64, i32, f64, i64, ctypes.POINTER(f64), ctypes.POINTER(f32)], i32),
+        "zha_rotary_apply": ([RP, i32, i32, i32, i32, i32, P, i64, P, i64, P, P, i64, P, i64, i32, P], i32),
+        "zha_paged_write": ([PP, RP, i32, P, i64, P, i64, P, i64, P, P, P, P, P, P, P], i32),
+        "zha_paged_workspace_bytes": ([PP, i32], sz),
+        "zha_paged_decode": ([PP, i32, P, P, P, P, P, P, P, P, P, P, P, P], i32),
         "zha_launch_count": ([], ctypes.c_uint64),
         "zha_profile_enable": ([i32], i32),
         "zha_profile_read": ([ctypes.c_char_p, i32, ctypes.POINTER(ctypes.c_double),
@@ -235,6 +267,249 @@ def topp_select(scores, counts, p, kept, dev_status=None, stream=None):
                                _p(dev_status), _stream(stream)), "zha_topp_select")
 
 
+# ---------------------------------------------------------------- paged caches and rotary positions
+
+def paged_config(batch, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, dtype="bf16", scale=0.0,
+                 window=0) -> PagedConfig:
+    dt = {"bf16": ZHA_BF16, "f32": ZHA_F32}.get(dtype, dtype)
+    c = PagedConfig(batch, n_q_heads, n_kv_heads, head_dim, dt, page_size, n_pages, max_pages, scale, window)
+    check(_lib.zha_paged_check_config(ctypes.byref(c)), "zha_paged_check_config")
+    return c
+
+
+def paged_workspace_bytes(cfg: PagedConfig, rows: int) -> int:
+    return int(_lib.zha_paged_workspace_bytes(ctypes.byref(cfg), int(rows)))
+
+
+def paged_workspace(cfg: PagedConfig, rows: int, device="cuda"):
+    """Zeroed scratch of paged_decode calls of up to `rows` rows (one call at a time)."""
+    n = paged_workspace_bytes(cfg, rows)
+    if n == 0:
+        raise ZhaError(1, "zha_paged_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _refuse(where: str, what: str):
+    raise ValueError(f"{where}: {what}")
+
+
+def _rows(t, where, name, heads, d, dtype, device):
+    """Token stride (elements) of a [n, heads, d] tensor whose heads are packed; the rest of its layout is refused."""
+    st = t.stride()
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype is not dtype or t.device != device:
+        _refuse(where, f"{name} must be a {dtype} tensor [n, {heads}, {d}] on {device}, got {t.dtype} "
+                       f"{tuple(t.shape)} on {t.device}")
+    if t.shape[0] and (st[2] != 1 or (heads > 1 and st[1] != d)):
+        _refuse(where, f"{name}'s heads must be packed (strides {st})")
+    return st[0] if t.shape[0] > 1 else heads * d
+
+
+def _int32(t, where, name, n, device):
+    """An int32 array of at least n entries; None passes."""
+    if t is not None and (t.dtype is not torch.int32 or t.device != device or t.numel() < n or not t.is_contiguous()):
+        _refuse(where, f"{name} must be a contiguous int32 tensor of at least {n} entries on {device}, got {t.dtype} "
+                       f"{tuple(t.shape)} on {t.device}")
+    return None if t is None else t.data_ptr()
+
+
+def _pool(t, where, name, cfg, device):
+    if (t.dtype is not cfg.torch_dtype or t.device != device or not t.is_contiguous()
+            or t.numel() != cfg.n_pages * cfg.n_kv_heads * cfg.page_size * cfg.head_dim):
+        _refuse(where, f"{name} must be a contiguous {cfg.torch_dtype} tensor [{cfg.n_pages}, {cfg.n_kv_heads}, "
+                       f"{cfg.page_size}, {cfg.head_dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _call(where, fn, device, stream, args):
+    """fn(*args, stream) on `device` (made current for the call where it is not), on its current stream by default."""
+    if device.type != "cuda":
+        _refuse(where, f"tensors must be on a CUDA device, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    if code != 0:
+        raise ZhaError(code, where)
+
+
+class Rotary:
+    """A rotary embedding: its frequency table (turns per position, fp64) on the device.
+
+    layout "half" pairs coordinates (i, i + rotary_dim/2), "interleaved" (2i, 2i + 1); scaling "none",
+    "linear", "ntk" or "yarn" by `factor` (from a context of original_len for YaRN)."""
+
+    def __init__(self, rotary_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_len=4096,
+                 device="cuda"):
+        kind = {"none": ZHA_ROPE_PLAIN, "linear": ZHA_ROPE_LINEAR, "ntk": ZHA_ROPE_NTK, "yarn": ZHA_ROPE_YARN}
+        lay = {"half": ZHA_ROPE_HALF, "interleaved": ZHA_ROPE_INTERLEAVED}
+        table = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+        m = ctypes.c_float()
+        check(_lib.zha_rotary_freqs(int(rotary_dim), float(base), kind.get(scaling, scaling), float(factor),
+                                    int(original_len), table, ctypes.byref(m)), "zha_rotary_freqs")
+        self.freq = torch.tensor(list(table), dtype=torch.float64).to(device)
+        self.desc = RotaryDesc(int(rotary_dim), lay.get(layout, layout), m.value, 0, self.freq.data_ptr())
+        self.ref = ctypes.byref(self.desc)
+
+
+def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
+    """Rotate q [n, Hq, d] and k [n, Hk, d] (either may be None; tokens may be strided) at int32 positions [n].
+    The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out)."""
+    where = "zha_rotary_apply"
+    one = q if q is not None else k
+    if one is None:
+        _refuse(where, "q or k is needed")
+    n, d, dt, dev = one.shape[0], one.shape[-1], one.dtype, one.device
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        _refuse(where, f"dtype {dt} is not supported")
+    args = []
+    heads = []
+    outs = []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            heads.append(0)
+            args.append((None, 0, None, 0))
+            outs.append(None)
+            continue
+        y = x if y is None else y
+        if x.dim() != 3 or x.shape[0] != n or y.shape != x.shape:
+            _refuse(where, f"{name} and {name}_out must be [{n}, heads, {d}]")
+        heads.append(x.shape[1])
+        args.append((x.data_ptr(), _rows(x, where, name, x.shape[1], d, dt, dev), y.data_ptr(),
+                     _rows(y, where, name + "_out", x.shape[1], d, dt, dev)))
+        outs.append(y)
+    (qp, qs, qo, qos), (kp, ks, ko, kos) = args
+    _call(where, _lib.zha_rotary_apply, dev, stream,
+          (rot.ref, d, ZHA_BF16 if dt is torch.bfloat16 else ZHA_F32, n, heads[0], heads[1], qp, qs, kp, ks,
+           _int32(positions, where, "positions", n, dev), qo, qos, ko, kos, 1 if transpose else 0))
+    return outs[0], outs[1]
+
+
+def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_map, lens_out=None, n_free_out=None,
+               dev_status=None, stream=None):
+    """Block tables, slots and lengths of a step with n_new[b] new tokens of sequence b (< 0: it ends).
+    token_map: {"positions", "slots", "seq_ids"} (one entry per row of the token buffer) and "cu" [batch + 1];
+    lens_out and n_free_out default to lens and n_free (in place)."""
+    where, dev, B = "zha_paged_plan", table.device, cfg.batch
+    rows = token_map["slots"].numel()
+    m = TokenMap(_int32(token_map["positions"], where, "positions", rows, dev),
+                 _int32(token_map["slots"], where, "slots", rows, dev),
+                 _int32(token_map["seq_ids"], where, "seq_ids", rows, dev),
+                 _int32(token_map["cu"], where, "cu", B + 1, dev), rows, 0)
+    _call(where, _lib.zha_paged_plan, dev, stream,
+          (ctypes.byref(cfg), _int32(table, where, "table", B * cfg.max_pages, dev),
+           _int32(lens, where, "lens", B, dev), _int32(n_new, where, "n_new", B, dev),
+           _int32(free_pages, where, "free_pages", cfg.n_pages, dev), _int32(n_free, where, "n_free", 1, dev),
+           _int32(lens if lens_out is None else lens_out, where, "lens_out", B, dev),
+           _int32(n_free if n_free_out is None else n_free_out, where, "n_free_out", 1, dev), ctypes.byref(m),
+           _int32(dev_status, where, "dev_status", 1, dev)))
+
+
+def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status=None,
+                stream=None):
+    """Rotate q and k_new [n, heads, d] and write k_new, v_new to their cache slots [n] (negative: skipped).
+    rot None: no rotation; q None: keys and values only."""
+    where, dev, dt, d = "zha_paged_write", k_pool.device, cfg.torch_dtype, cfg.head_dim
+    n = k_new.shape[0]
+    if v_new.shape[0] != n or (q is not None and (q.shape[0] != n or q_out is None or q_out.shape != q.shape
+                                                  or not q_out.is_contiguous())):
+        _refuse(where, f"q, q_out (contiguous) and v_new must have k_new's {n} tokens")
+    hq, hkv = cfg.n_q_heads, cfg.n_kv_heads
+    if q is not None:
+        _rows(q_out, where, "q_out", hq, d, dt, dev)
+    _call(where, _lib.zha_paged_write, dev, stream,
+          (ctypes.byref(cfg), None if rot is None else rot.ref, n, None if q is None else q.data_ptr(),
+           0 if q is None else _rows(q, where, "q", hq, d, dt, dev), k_new.data_ptr(),
+           _rows(k_new, where, "k_new", hkv, d, dt, dev), v_new.data_ptr(),
+           _rows(v_new, where, "v_new", hkv, d, dt, dev), _int32(positions, where, "positions", n, dev),
+           _int32(slots, where, "slots", n, dev), None if q is None else q_out.data_ptr(),
+           _pool(k_pool, where, "k_pool", cfg, dev), _pool(v_pool, where, "v_pool", cfg, dev),
+           _int32(dev_status, where, "dev_status", 1, dev)))
+    return q_out
+
+
+def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspace, lse=None, seq_ids=None,
+                 positions=None, dev_status=None, stream=None):
+    """Attention of rows q [n, Hq, d] over the paged cache into out (and lse [n, Hq] fp32). Row r is of sequence
+    seq_ids[r] (default r; negative: left as it is) and attends tokens 0 .. positions[r] (default: all)."""
+    where, dev, dt = "zha_paged_decode", q.device, cfg.torch_dtype
+    n, shape = q.shape[0], (q.shape[0], cfg.n_q_heads, cfg.head_dim)
+    if (q.shape != shape or out.shape != shape or q.dtype is not dt or out.dtype is not dt or out.device != dev
+            or not q.is_contiguous() or not out.is_contiguous()):
+        _refuse(where, f"q and out must be contiguous {dt} tensors {shape} on one device")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2] or lse.device != dev
+                            or not lse.is_contiguous()):
+        _refuse(where, f"lse must be a contiguous fp32 tensor {shape[:2]}")
+    if (workspace.device != dev or not workspace.is_contiguous()
+            or workspace.numel() * workspace.element_size() < _lib.zha_paged_workspace_bytes(ctypes.byref(cfg), n)):
+        _refuse(where, f"the workspace must hold paged_workspace_bytes(cfg, {n}) bytes on {dev}")
+    _call(where, _lib.zha_paged_decode, dev, stream,
+          (ctypes.byref(cfg), n, q.data_ptr(), _pool(k_pool, where, "k_pool", cfg, dev),
+           _pool(v_pool, where, "v_pool", cfg, dev), _int32(table, where, "table", cfg.batch * cfg.max_pages, dev),
+           _int32(lens, where, "lens", cfg.batch, dev), _int32(seq_ids, where, "seq_ids", n, dev),
+           _int32(positions, where, "positions", n, dev), out.data_ptr(), None if lse is None else lse.data_ptr(),
+           workspace.data_ptr(), _int32(dev_status, where, "dev_status", 1, dev)))
+    return out
+
+
+class PagedCache:
+    """Device state of one layer's paged cache: pools, block table, lengths, free pages, a step's token map and
+    buffers, status. max_tokens is the size of a step's token buffer; shorter steps leave its tail unused.
+
+    step() runs plan, write and decode; everything stays on the device, so a step can be captured into a CUDA
+    graph (n_new, q, k_new, v_new are then the captured buffers). The cache serves one step at a time."""
+
+    def __init__(self, cfg: PagedConfig, max_tokens: int, rot: Rotary | None = None, device="cuda"):
+        self.cfg, self.rot = cfg, rot
+        kw = dict(dtype=torch.int32, device=device)
+        shape = (cfg.n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
+        self.k_pool = torch.zeros(shape, dtype=cfg.torch_dtype, device=device)
+        self.v_pool = torch.zeros(shape, dtype=cfg.torch_dtype, device=device)
+        self.table = torch.full((cfg.batch, cfg.max_pages), -1, **kw)
+        self.lens = torch.zeros(cfg.batch, **kw)
+        self.free_pages = torch.arange(cfg.n_pages - 1, -1, -1, **kw)     # page 0 is on top
+        self.n_free = torch.full((1,), cfg.n_pages, **kw)
+        self.token_map = {"positions": torch.zeros(max_tokens, **kw), "slots": torch.full((max_tokens,), -1, **kw),
+                          "seq_ids": torch.full((max_tokens,), -1, **kw), "cu": torch.zeros(cfg.batch + 1, **kw)}
+        rows = (max_tokens, cfg.n_q_heads, cfg.head_dim)
+        self.q = torch.zeros(rows, dtype=cfg.torch_dtype, device=device)
+        self.out = torch.zeros(rows, dtype=cfg.torch_dtype, device=device)
+        self.lse = torch.zeros(rows[:2], dtype=torch.float32, device=device)
+        self.workspace = paged_workspace(cfg, max_tokens, device)
+        self.status = torch.zeros(1, **kw)
+
+    def plan(self, n_new, stream=None):
+        """Room for n_new[b] more tokens of each sequence (< 0: it ends); fills the token map."""
+        paged_plan(self.cfg, self.table, self.lens, n_new, self.free_pages, self.n_free, self.token_map,
+                   dev_status=self.status, stream=stream)
+
+    def write(self, q, k_new, v_new, stream=None):
+        """Rotated queries into self.q, rotated keys and values into the cache, for the planned token rows."""
+        m = self.token_map
+        paged_write(self.cfg, self.rot, q, k_new, v_new, m["positions"], m["slots"], self.q, self.k_pool, self.v_pool,
+                    dev_status=self.status, stream=stream)
+
+    def attend(self, stream=None):
+        """Each planned token's attention over its sequence up to itself: (out, lse), rows as in the token map."""
+        m = self.token_map
+        paged_decode(self.cfg, self.q, self.k_pool, self.v_pool, self.table, self.lens, self.out, self.workspace,
+                     lse=self.lse, seq_ids=m["seq_ids"], positions=m["positions"], dev_status=self.status,
+                     stream=stream)
+        return self.out, self.lse
+
+    def step(self, n_new, q, k_new, v_new, stream=None):
+        """q [max_tokens, Hq, d], k_new, v_new [max_tokens, Hkv, d]: the step's token rows, before rotation."""
+        self.plan(n_new, stream)
+        self.write(q, k_new, v_new, stream)
+        return self.attend(stream)
+
+    def check_status(self, where="device"):
+        code = int(self.status.item())
+        if code:
+            self.status.zero_()
+            raise ZhaError(code, where)
+
+
 def wait_expiry_check(kind: int, limit_cycles: int, dev_status, stream=None):
     """Run one of the library's bounded device waits on a condition nothing
     satisfies (ZHA_WAIT_ROW_BARRIER or ZHA_WAIT_MBARRIER), giving up after
@@ -269,12 +544,15 @@ class DecodeGraph:
 
     Every pointer, grid size and p is fixed at capture; the cache lengths live
     on the device, so one graph serves every later step. Inputs are copied into
-    the graph's own q / k_new / v_new buffers before each replay."""
+    the graph's own q / k_new / v_new buffers before each replay. With `rot` (a
+    Rotary) q and k_new are given before rotation: staging them turns them to
+    the new token's position, lens[b]."""
 
-    def __init__(self, cfg, buf, K, V, refs, lens, p):
+    def __init__(self, cfg, buf, K, V, refs, lens, p, rot=None):
         B, Hq, Hkv, d = cfg.batch, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
         dt = cfg.torch_dtype
         dev = K.device
+        self.rot, self.lens = rot, lens
         self.q = torch.zeros((B, Hq, d), dtype=dt, device=dev)
         self.k_new = torch.zeros((B, Hkv, d), dtype=dt, device=dev)
         self.v_new = torch.zeros((B, Hkv, d), dtype=dt, device=dev)
@@ -292,7 +570,12 @@ class DecodeGraph:
 
     def stage(self, q, k_new, v_new):
         """Put a step's inputs into the graph's own buffers (one multi-tensor
-        copy); a caller that produces them there directly skips this."""
+        copy, or the rotation and a copy of v_new); a caller that produces them
+        there directly skips this."""
+        if self.rot is not None:
+            rotary(self.rot, q, k_new, self.lens, self.q, self.k_new)
+            self.v_new.copy_(v_new, non_blocking=True)
+            return
         torch._foreach_copy_([self.q, self.k_new, self.v_new], [q, k_new, v_new], non_blocking=True)
 
     def replay(self):
