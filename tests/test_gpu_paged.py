@@ -371,7 +371,9 @@ def test_decode_special_values(zha, dt):
     assert torch.equal(lse[1], good[1][1])
     assert torch.all(torch.isfinite(out[2])) and torch.all(torch.isfinite(lse[2]))
     want = c.v[c.table[3, 3], 0, 5]
-    assert torch.equal(out[3], want.expand(2, 64))
+    # bf16: exactly. fp32 values are taken as two tf32 parts of 11 bits: the first leaves at most 2^-11 |v|, the second
+    # at most 2^-11 of that; their sum is rounded once more (2^-24): below 2^-21 |v|
+    assert torch.all((out[3] - want).abs() <= (0.0 if dt is BF16 else 2.0 ** -21) * want.abs())
     assert torch.equal(out[4], good[0][4])
 
 
