@@ -14,16 +14,21 @@
 // 16 KB of K and 16 KB of V; all groups' tiles form one list, and every CTA
 // (two per SM) takes an equal contiguous part of it, whatever the rows'
 // lengths are. A group that lies inside one CTA's part is written directly;
-// of any other, each CTA that holds a piece leaves (m, l, o) in the workspace
-// and the last one to arrive joins the pieces in their order.
+// of any other, each CTA that holds a piece leaves (m, l, o) in the workspace,
+// and the last to arrive joins the pieces in their order (in two levels where
+// they are many).
 //
-// Inside a CTA the copies of the next two tiles (16-byte cp.async gathers by
-// page, across group borders) are in flight while one is computed: S = Q K^T
-// with each of the four warps on a quarter of the tile's tokens, the common
-// row maximum and the weights through shared memory, then O += P V with each
-// warp on a quarter of the head's coordinates. So O is spread over the CTA
-// and a group's end needs no exchange, which keeps short rows cheap.
+// Inside a CTA a fifth warp walks the tiles ahead of the other four: it looks
+// their pages up and copies runs of up to 16 rows of a page by TMA into a ring
+// of three tiles, across the groups' borders. The four warps compute
+// S = Q K^T, each on a quarter of the tile's tokens, share the row maxima and
+// the weights through shared memory, and then O += P V, each on a quarter of
+// the head's coordinates: O is spread over the CTA and a group's end needs no
+// exchange, which keeps short rows cheap.
 #include "zha_paged.cuh"
+#include <type_traits>
+
+#include "zha_tc.cuh"
 
 namespace zha {
 
@@ -31,14 +36,16 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kMath = kWarps * 32, kThreads = kMath + 32;
 constexpr int kStages = 3;
 constexpr int kRows = 16;                // query heads of a group, padded to the MMA's rows
 constexpr int kTileBytes = 16384;        // of K, and of V
 constexpr int kMaxWorkers = 148 * 2;
 constexpr int kMinTiles = 4;             // tiles of a CTA's part at least
-constexpr int kOffSlots = 4, kDescSlots = 8;
-constexpr int kJoin = 64;                // pieces joined at a time
+constexpr int kBox = 16;                 // rows of a page copied at a time, at most
+constexpr int kDirect = 16;              // pieces of a group joined at once; more in two levels
+constexpr int kSetMax = 24;              // ceil(sqrt(kMaxWorkers)) rounded up to a multiple of 8
+constexpr long long kWaitCycles = 4000000000ll;   // ~2 s: a wait that long is an error
 
 // The tokens [lo, hi) that row r attends and the sequence they belong to
 // (-1: the row is left as it is).
@@ -70,13 +77,6 @@ __device__ __forceinline__ RowSpan row_span(const PagedAttnArgs &a, int r) {
     return s;
 }
 
-__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -106,10 +106,36 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
 // main + corr, or main alone where the correction is not finite: the small
 // parts of a split operand would turn an infinite factor into NaN.
 __device__ __forceinline__ float with_correction(float main, float corr) {
     return fabsf(corr) <= 3.0e38f ? main + corr : main;
+}
+// barriers of the four computing warps (the copying warp takes no part)
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+__device__ __forceinline__ bool math_any(bool x) {
+    int r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}\n"
+                 : "=r"(r) : "r"((int)x) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+// arrive on an mbarrier once this thread's cp.async copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %3, %4}], [%2];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(w)
+        : "memory");
 }
 
 // A piece of a group in the workspace: (m, l) of its G heads, padded to whole
@@ -117,35 +143,44 @@ __device__ __forceinline__ float with_correction(float main, float corr) {
 __host__ __device__ __forceinline__ int piece_ml(int G) { return (2 * G + 3) & ~3; }
 __host__ __device__ __forceinline__ int piece_floats(int G, int d) { return piece_ml(G) + G * d; }
 
-// One tile of a group.
+// One tile of a group, as the copying warp describes it to the others.
 struct Tile {
     int r, kvh;
     int len;          // tiles of the group
     int flags;
     int64_t g0;       // the group's first tile in the list of all tiles
+    int base, lo, hi; // first token, and the tokens the row attends
+    uint32_t bad[4];  // tokens whose page number is no page
 };
-enum { kFirst = 1, kLast = 2, kWhole = 4 };   // of this CTA's piece of the group; the piece is the group
+// of this CTA's piece of the group: its first and last tile; the piece is the group; some token is not attended
+enum { kFirst = 1, kLast = 2, kWhole = 4, kEdge = 8 };
 
 template <typename T, int D>
 struct Shared {
     static constexpr int TT = kTileBytes / (D * (int)sizeof(T));   // tokens of a tile
-    // P as [16][TT] high parts, then low parts, rows padded against bank conflicts
-    static constexpr int PS = sizeof(T) == 2 ? TT + 8 : TT + 4;
+    static constexpr int PS = TT + 8;    // a row of P, padded against bank conflicts
+    // K then V of a tile: blocks of 8 tokens, [D * sizeof(T) / 128][8][128 bytes], 16-byte chunks
+    // XOR-swizzled by the row (the 128-byte swizzle of a TMA copy)
     uint8_t ring[kStages][2 * kTileBytes];
+    // P in two parts: weights keep 16 (bf16) or 22 (tf32) bits; one bf16 part alone would cost half an
+    // ulp of the output
+    typedef typename std::conditional<sizeof(T) == 2, __nv_bfloat16, float>::type PT;
     union {
-        alignas(16) T p[2][kRows][PS];
-        float weight[kJoin][kRows];
+        alignas(16) PT p[2][kRows][PS];
+        float weight[kSetMax][kRows];
     };
-    int64_t off[kOffSlots][TT];          // byte offset of each token's row in its pool, -1: none
-    Tile tile[kDescSlots];
-    float mx[kWarps * 2][kRows], sum[kWarps * 2][kRows];
-    int64_t scan[kWarps];
+    Tile tile[kStages];
+    float mx[2 * kWarps][kRows], sum[2 * kWarps][kRows];
+    int64_t scan[kThreads / 32];
     int64_t start_before;
-    int start_row, last;
+    uint64_t full[kStages], empty[kStages];
+    int start_row, last, abort;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a, float *parts, int32_t *arrived) {
+template <typename T, int D, bool kTma>
+__global__ void __launch_bounds__(kThreads, 2)
+paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  float *parts, int32_t *arrived) {
     using S = Shared<T, D>;
     constexpr bool kBf16 = sizeof(T) == 2;
     constexpr int TT = S::TT;
@@ -155,18 +190,25 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gq = lane >> 2, t4 = lane & 3;
+    const int box = min(1 << a.lps, kBox);      // rows of a page copied at a time; tiles begin on a box
+    volatile int *abort = &sm.abort;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.full[i]), kTma ? 1 : 33);
+            mbar_init(smem_u32(&sm.empty[i]), kWarps);
+        }
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        fence_proxy_async_smem();
+    }
     pdl_wait();
 
     // ---- this CTA's part [w0, w1) of the list of all tiles, and the row it begins in
     const int per = (a.rows + kThreads - 1) / kThreads;
     const int ra = min(tid * per, a.rows), rb = min(ra + per, a.rows);
-    auto tiles_of = [&](int r) {
-        const RowSpan s = row_span(a, r);
-        return (s.hi - s.lo + TT - 1) / TT;
-    };
+    auto tiles_of = [&](const RowSpan &s) { return s.hi > s.lo ? (s.hi - (s.lo & -box) + TT - 1) / TT : 0; };
     int64_t mine = 0;
-    for (int r = ra; r < rb; ++r) mine += tiles_of(r);
+    for (int r = ra; r < rb; ++r) mine += tiles_of(row_span(a, r));
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -177,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     __syncthreads();
     int64_t before = incl - mine, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += sm.scan[w];
         all += sm.scan[w];
     }
@@ -187,507 +229,618 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     const int64_t w0 = (int)blockIdx.x < P ? W * blockIdx.x / P : 0;
     const int64_t w1 = (int)blockIdx.x < P ? W * (blockIdx.x + 1) / P : 0;
     const int n = (int)(w1 - w0);
-
-    if (n > 0) {
-        if (w0 >= before * a.Hkv && w0 < (before + mine) * a.Hkv) {
-            int64_t at = before;
-            for (int r = ra; r < rb; ++r) {
-                const int t = tiles_of(r);
-                if (w0 < (at + t) * a.Hkv) {
-                    sm.start_row = r;
-                    sm.start_before = at;
-                    break;
-                }
-                at += t;
+    if (n > 0 && w0 >= before * a.Hkv && w0 < (before + mine) * a.Hkv) {
+        int64_t at = before;
+        for (int r = ra; r < rb; ++r) {
+            const int t = tiles_of(row_span(a, r));
+            if (w0 < (at + t) * a.Hkv) {
+                sm.start_row = r;
+                sm.start_before = at;
+                break;
             }
+            at += t;
         }
-        __syncthreads();
+    }
+    __syncthreads();
 
-        // ---- the reading end: which tile's pages are looked up next
-        int c_r = sm.start_row, c_len = tiles_of(c_r);
+    if (warp == kWarps) {
+        // ================= the copying warp
+        if (n == 0) return;
+        int c_r = sm.start_row;
+        RowSpan span = row_span(a, c_r);
+        int c_len = tiles_of(span);
         int64_t c_g0 = sm.start_before * a.Hkv;
         int c_kvh = (int)((w0 - c_g0) / c_len);
         c_g0 += (int64_t)c_kvh * c_len;
         int c_i = (int)(w0 - c_g0);
-        RowSpan c_span = row_span(a, c_r);
-        // looks up the page of this thread's token of tile k (of this CTA's part), leaves the tile's
-        // description, and moves on; returns the page (-1: no token)
-        int look_in = 0;                   // row inside the page, head included
-        auto look = [&](int k) -> int {
-            int page = -1;
-            if (k < n) {
-                const int pos = c_span.lo + c_i * TT + tid;
-                if (tid < TT && pos < c_span.hi) {
-                    page = __ldg(a.table + (int64_t)c_span.seq * a.max_pages + (pos >> a.lps));
-                    look_in = (c_kvh << a.lps) + (pos & ((1 << a.lps) - 1));
-                }
-                if (tid == 0) {
-                    Tile d;
-                    d.r = c_r;
-                    d.kvh = c_kvh;
-                    d.len = c_len;
-                    d.g0 = c_g0;
-                    const bool first = k == 0 || c_i == 0, last = k == n - 1 || c_i == c_len - 1;
-                    const bool whole = c_g0 >= w0 && c_g0 + c_len <= w1;
-                    d.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (whole ? kWhole : 0);
-                    sm.tile[k % kDescSlots] = d;
-                }
-                if (++c_i == c_len && k + 1 < n) {
-                    c_i = 0;
-                    c_g0 += c_len;
-                    if (++c_kvh == a.Hkv) {
-                        c_kvh = 0;
-                        do {
-                            c_span = row_span(a, ++c_r);
-                            c_len = (c_span.hi - c_span.lo + TT - 1) / TT;
-                        } while (c_len == 0);
+        // a lane's pages: its box of the tile (TMA), or its tokens lane, lane + 32, ... (small pages)
+        constexpr int NP = kTma ? 1 : TT / 32;
+        const int boxes = TT / box;
+        const int lbox = 31 - __clz(box);
+        int page[NP];
+        auto token = [&](int i) { return (span.lo & -box) + c_i * TT + (kTma ? lane * box : lane + 32 * i); };
+        auto look = [&]() {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int pos = token(i);
+                page[i] = (!kTma || lane < boxes) && pos < span.hi
+                              ? __ldg(a.table + (int64_t)span.seq * a.max_pages + (pos >> a.lps)) : -1;
+            }
+        };
+        look();
+        int k = 0;
+        for (; k < n; ++k) {
+            const int st = k % kStages;
+            Tile d;
+            d.r = c_r;
+            d.kvh = c_kvh;
+            d.len = c_len;
+            d.g0 = c_g0;
+            d.base = (span.lo & -box) + c_i * TT;
+            d.lo = span.lo;
+            d.hi = span.hi;
+            d.flags = ((k == 0 || c_i == 0) ? kFirst : 0) | ((k == n - 1 || c_i == c_len - 1) ? kLast : 0) |
+                      ((c_g0 >= w0 && c_g0 + c_len <= w1) ? kWhole : 0) |
+                      ((d.base < d.lo || d.base + TT > d.hi) ? kEdge : 0);
+            d.bad[0] = d.bad[1] = d.bad[2] = d.bad[3] = 0;
+            int64_t row[NP];               // first row of the copy in its pool, -1: none
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int pos = token(i);
+                const bool in = (!kTma || lane < boxes) && pos < span.hi, ok = in && (unsigned)page[i] < (unsigned)a.n_pages;
+                row[i] = ok ? (((int64_t)page[i] * a.Hkv + c_kvh) << a.lps) + (pos & ((1 << a.lps) - 1)) : -1;
+                const uint32_t bad = __ballot_sync(0xffffffffu, in && !ok);
+                if (bad) {
+                    if (in && !ok) set_status(a.status, ZHA_ERR_INVALID_ARG);
+                    d.flags |= kEdge;
+                    if constexpr (kTma) {
+#pragma unroll
+                        for (int w = 0; w < (TT + 31) / 32; ++w)
+                            for (int t = 0; t < 32; ++t)
+                                if ((bad >> ((32 * w + t) >> lbox)) & 1u) d.bad[w] |= 1u << t;
+                    } else {
+                        d.bad[i] = bad;
                     }
                 }
             }
-            return page;
-        };
-        const int64_t page_rows = (int64_t)a.Hkv << a.lps;
-        auto put_off = [&](int k, int page, int in, bool asked) {
-            if (tid < TT) {
-                const bool ok = (unsigned)page < (unsigned)a.n_pages;
-                if (asked && !ok) set_status(a.status, ZHA_ERR_INVALID_ARG);
-                sm.off[k % kOffSlots][tid] = ok ? (page * page_rows + in) * ROWB : -1;
-            }
-        };
-        const uint32_t ring = smem_at(sm.ring);
-        const char *kpool = static_cast<const char *>(a.kpool), *vpool = static_cast<const char *>(a.vpool);
-        auto issue = [&](int k) {
-            if (k < n) {
-                const uint32_t kb = ring + (k % kStages) * 2 * kTileBytes, vb = kb + kTileBytes;
-#pragma unroll
-                for (int j = 0; j < TT * CH / kThreads; ++j) {
-                    const int c = tid + j * kThreads, row = c / CH, ch = c % CH;
-                    const int64_t o = sm.off[k % kOffSlots][row];
-                    const bool ok = o >= 0;
-                    const int64_t at = (ok ? o : 0) + ch * 16;
-                    // 16-byte chunks are permuted in a row so that the reads below meet no bank twice
-                    const int ks = kBf16 ? (ch ^ (row & 7)) : (ch ^ ((row & 1) << 2));
-                    const int vs = kBf16 ? (ch ^ (row & 7)) : (ch ^ ((row & 3) << 1));
-                    cp16(kb + row * ROWB + ks * 16, kpool + at, ok);
-                    cp16(vb + row * ROWB + vs * 16, vpool + at, ok);
+            // the next tile's pages are on their way while this one waits for its place
+            if (++c_i == c_len && k + 1 < n) {
+                c_i = 0;
+                c_g0 += c_len;
+                if (++c_kvh == a.Hkv) {
+                    c_kvh = 0;
+                    do {
+                        span = row_span(a, ++c_r);
+                        c_len = tiles_of(span);
+                    } while (c_len == 0);
                 }
             }
-            cp_commit();
-        };
-
-        // ---- before the first tile: pages of four tiles, copies of two
-        int next_page, next_in;
-        bool next_asked;
-        {
-            int pg[3], in[3];
-            bool as[3];
+            if (k + 1 < n) look();
+            if (k >= kStages && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.empty[st]), (k / kStages - 1) & 1,
+                                                                           kWaitCycles, abort, a.status)))
+                break;
+            const uint32_t kb = smem_u32(sm.ring[st]), vb = kb + kTileBytes, full = smem_u32(&sm.full[st]);
+            if (lane == 0) sm.tile[st] = d;
+            if constexpr (kTma) {
+                const bool ok = row[0] >= 0;
+                const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
+                if (lane == 0) mbar_expect_tx(full, cnt * 2u * (uint32_t)box * ROWB);
+                __syncwarp();
+                if (ok) {
+                    const uint32_t off = (uint32_t)lane * box * ROWB;
+                    tma_load_4d(kb + off, &kmap, (int)(row[0] >> 3), full);
+                    tma_load_4d(vb + off, &vmap, (int)(row[0] >> 3), full);
+                }
+            } else {
+#pragma unroll 4
+                for (int j = 0; j < TT * CH / 32; ++j) {
+                    const int tok = (j * 32) / CH + lane / CH, ch = (j * 32) % CH + lane % CH;
+                    const int64_t rw = __shfl_sync(0xffffffffu, row[0], tok & 31);
+                    int64_t r2 = rw;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                as[k] = k < n && tid < TT && c_span.lo + c_i * TT + tid < c_span.hi;
-                pg[k] = look(k);
-                in[k] = look_in;
+                    for (int i = 1; i < NP; ++i) {
+                        const int64_t x = __shfl_sync(0xffffffffu, row[i], tok & 31);
+                        if ((tok >> 5) == i) r2 = x;
+                    }
+                    const bool ok = r2 >= 0;
+                    const int64_t at = (ok ? r2 : 0) * ROWB + ch * 16;
+                    const uint32_t off = (tok >> 3) * 8 * ROWB + (ch >> 3) * 1024 + (tok & 7) * 128 + (((ch & 7) ^ (tok & 7)) << 4);
+                    cp16(kb + off, static_cast<const char *>(a.kpool) + at, ok);
+                    cp16(vb + off, static_cast<const char *>(a.vpool) + at, ok);
+                }
+                cp_arrive(full);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
             }
-            next_asked = 3 < n && tid < TT && c_span.lo + c_i * TT + tid < c_span.hi;
-            next_page = look(3);
-            next_in = look_in;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) put_off(k, pg[k], in[k], as[k]);
         }
-        __syncthreads();
-        issue(0);
-        issue(1);
+        // given up: the copies in flight still land before the CTA may end
+        if (k < n)
+            for (int j = k < kStages ? 0 : k - kStages; j < k; ++j)
+                mbar_wait_bounded(smem_u32(&sm.full[j % kStages]), (j / kStages) & 1, kWaitCycles, nullptr, a.status);
+        return;
+    }
 
-        // Q fragments: bf16 as they are; fp32 split in two tf32 parts
-        constexpr int KS = kBf16 ? D / 16 : D / 8;
-        uint32_t qf[KS][4], ql[kBf16 ? 1 : KS][4];
-        float o[NJ][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // ================= the computing warps
+    const int gq = lane >> 2, t4 = lane & 3;
+    // Q fragments: bf16 as they are; fp32 split in two tf32 parts
+    constexpr int KS = kBf16 ? D / 16 : D / 8;
+    uint32_t qf[KS][4], ql[kBf16 ? 1 : KS][4];
+    float o[NJ][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        const float s2 = a.s * kLog2e;
+    for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    const float s2 = a.s * kLog2e;
+    const int tok0 = warp * (TT / 4);
 
-        auto load_q = [&](int r, int kvh) {
-            const T *q = static_cast<const T *>(a.q) + ((int64_t)r * a.Hq + kvh * a.G) * D;
+    auto load_q = [&](int r, int kvh) {
+        const T *q = static_cast<const T *>(a.q) + ((int64_t)r * a.Hq + kvh * a.G) * D;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int h = gq + 8 * half;
-                const bool ok = h < a.G;
-                if constexpr (kBf16) {
-                    const uint32_t *row = reinterpret_cast<const uint32_t *>(q + (ok ? h : 0) * D);
+        for (int half = 0; half < 2; ++half) {
+            const int h = gq + 8 * half;
+            const bool ok = h < a.G;
+            if constexpr (kBf16) {
+                const uint32_t *row = reinterpret_cast<const uint32_t *>(q + (ok ? h : 0) * D);
 #pragma unroll
-                    for (int st = 0; st < KS; ++st) {
-                        qf[st][half] = ok ? row[st * 8 + t4] : 0u;
-                        qf[st][2 + half] = ok ? row[st * 8 + 4 + t4] : 0u;
-                    }
-                } else {
-                    // coordinates of 16 are dealt to the k slots so that a lane's are 4 in a row
-                    const float4 *row = reinterpret_cast<const float4 *>(q + (ok ? h : 0) * D);
+                for (int st = 0; st < KS; ++st) {
+                    qf[st][half] = ok ? row[st * 8 + t4] : 0u;
+                    qf[st][2 + half] = ok ? row[st * 8 + 4 + t4] : 0u;
+                }
+            } else {
+                // coordinates of 16 are dealt to the k slots so that a lane's are 4 in a row
+                const float4 *row = reinterpret_cast<const float4 *>(q + (ok ? h : 0) * D);
 #pragma unroll
-                    for (int st = 0; st < KS; st += 2) {
-                        const float4 x = ok ? row[st * 2 + t4] : make_float4(0.f, 0.f, 0.f, 0.f);
-                        split_tf32(x.x, qf[st][half], ql[st][half]);
-                        split_tf32(x.y, qf[st][2 + half], ql[st][2 + half]);
-                        split_tf32(x.z, qf[st + 1][half], ql[st + 1][half]);
-                        split_tf32(x.w, qf[st + 1][2 + half], ql[st + 1][2 + half]);
-                    }
+                for (int st = 0; st < KS; st += 2) {
+                    const float4 x = ok ? row[st * 2 + t4] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    split_tf32(x.x, qf[st][half], ql[st][half]);
+                    split_tf32(x.y, qf[st][2 + half], ql[st][2 + half]);
+                    split_tf32(x.z, qf[st + 1][half], ql[st + 1][half]);
+                    split_tf32(x.w, qf[st + 1][2 + half], ql[st + 1][2 + half]);
                 }
             }
-        };
-        // this lane's coordinate of column c (0, 1) of O's column block j
-        auto dim_of = [&](int j, int c) {
-            return warp * (D / 4) + (kBf16 ? 8 * j + 2 * t4 + c : (2 * t4 + c) * NJ + j);
-        };
+        }
+    };
+    // the token (of its 8) of column c (0, 1) of a lane's S, and the coordinate of column c of its O block j.
+    // fp32: tokens and coordinates are dealt to the MMAs' columns so that 16-byte reads meet no bank twice.
+    auto tok_of = [&](int c) { return kBf16 ? 2 * t4 + c : t4 + 4 * c; };
+    auto dim_of = [&](int j, int c) { return warp * (D / 4) + (kBf16 ? 8 * j + 2 * t4 + c : (2 * t4 + c) * NJ + j); };
+    // byte offsets of this lane's reads of K (two values of bit 2 of the chunk) and of V
+    uint32_t ko[2], vo[kBf16 ? NJ / 2 : 2];
+    {
+        const int r = kBf16 ? lane & 7 : (gq >> 1) | ((gq & 1) << 2), c = kBf16 ? lane >> 3 : t4;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) ko[b] = (tok0 >> 3) * 8 * ROWB + r * 128 + (((4 * b + c) ^ r) << 4);
+        if constexpr (kBf16) {
+#pragma unroll
+            for (int jp = 0; jp < NJ / 2; ++jp) {
+                const int ch = warp * (D / 32) + 2 * jp + (lane >> 4), rv = lane & 7;
+                vo[jp] = ((lane >> 3) & 1) * 8 * ROWB + (ch >> 3) * 1024 + rv * 128 + (((ch & 7) ^ rv) << 4);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int byte = (warp * (D / 4) + gq * NJ) * 4, ch = byte >> 4, rv = 2 * t4 + e;
+                vo[e] = (ch >> 3) * 1024 + rv * 128 + (((ch & 7) ^ rv) << 4) + (byte & 15);
+            }
+        }
+    }
 
-        for (int it = 0; it < n; ++it) {
-            cp_wait<1>();
-            __syncthreads();               // tile `it` has landed; everyone is done with tile it - 1
-            issue(it + 2);
-            put_off(it + 3, next_page, next_in, next_asked);
-            next_asked = it + 4 < n && tid < TT && c_span.lo + c_i * TT + tid < c_span.hi;
-            next_page = look(it + 4);
-            next_in = look_in;
-            const Tile d = sm.tile[it % kDescSlots];
-            if (d.flags & kFirst) load_q(d.r, d.kvh);
-            const uint8_t *kt = sm.ring[it % kStages], *vt = kt + kTileBytes;
-            const int64_t *off = sm.off[it % kOffSlots];
-            const int tok0 = warp * (TT / 4);
+    // Joins cnt pieces, the i-th in workspace slot slot(i): all heads' statistics, then o. The result goes to
+    // the group's output, or back into the workspace at `to`.
+    auto join = [&](int cnt, auto slot, int64_t head, float *to) {
+        auto piece = [&](int i) { return parts + (int64_t)slot(i) * piece_floats(a.G, D); };
+        const int jh = tid & 15, ji = tid >> 4;
+        float2 ml[kSetMax / 8];
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int e = 0; e < kSetMax / 8; ++e) {
+            const int i = ji + 8 * e;
+            ml[e] = i < cnt && jh < a.G ? __ldcg(reinterpret_cast<const float2 *>(piece(i)) + jh) : make_float2(-INFINITY, 0.f);
+            M = max_nan(M, ml[e].x);
+        }
+        sm.mx[ji][jh] = M;
+        math_sync();
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) M = max_nan(M, sm.mx[w][jh]);
+#pragma unroll
+        for (int e = 0; e < kSetMax / 8; ++e) {
+            const float f = ml[e].x == -INFINITY ? 0.f : ex2(ml[e].x - M);
+            sm.weight[ji + 8 * e][jh] = f;
+            L += f == 0.f ? 0.f : ml[e].y * f;
+        }
+        sm.sum[ji][jh] = L;
+        math_sync();
+        auto total = [&](int h) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) s += sm.sum[w][h];
+            return s;
+        };
+        constexpr int ITEMS = kRows * D / 4 / kMath;
+        float4 acc[ITEMS];
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int items = a.G * (D / 4);
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) {
+            const float4 *src = reinterpret_cast<const float4 *>(piece(i) + piece_ml(a.G));
+#pragma unroll
+            for (int e = 0; e < ITEMS; ++e) {
+                const int at = tid + e * kMath;
+                if (at < items) {
+                    const float4 v = __ldcg(src + at);
+                    const float f = sm.weight[i][at / (D / 4)];
+                    // a piece without weight may hold anything
+                    acc[e].x = f == 0.f ? acc[e].x : fmaf(v.x, f, acc[e].x);
+                    acc[e].y = f == 0.f ? acc[e].y : fmaf(v.y, f, acc[e].y);
+                    acc[e].z = f == 0.f ? acc[e].z : fmaf(v.z, f, acc[e].z);
+                    acc[e].w = f == 0.f ? acc[e].w : fmaf(v.w, f, acc[e].w);
+                }
+            }
+        }
+        if (to) math_sync();               // everyone has read piece 0, which the result replaces
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) {
+            const int at = tid + e * kMath, h = at / (D / 4);
+            if (at >= items) continue;
+            if (to) {
+                reinterpret_cast<float4 *>(to + piece_ml(a.G))[at] = acc[e];
+            } else {
+                const float l = total(h), v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
+                float y[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = l == 0.f ? 0.f : v[c] / l;
+                store_vec<4>(static_cast<T *>(a.out) + head * D + (int64_t)at * 4, y);
+            }
+        }
+        if (ji == 0 && jh < a.G) {
+            const float l = total(jh);
+            if (to) reinterpret_cast<float2 *>(to)[jh] = make_float2(M, l);
+            else if (a.lse) a.lse[head + jh] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+        }
+    };
+    // Announces this CTA's piece (or set of pieces) at a counter; true in the CTA that is the last of `of`.
+    auto arrive = [&](int32_t *counter, int of) {
+        __threadfence();
+        math_sync();
+        if (tid == 0) {
+            sm.last = atomicAdd(counter, 1) == of - 1;
+            if (sm.last) *counter = 0;
+        }
+        math_sync();
+        const bool last = sm.last;
+        if (last) __threadfence();
+        return last;
+    };
 
-            // ---- S = Q K^T of this warp's tokens
-            float x[NT][4];
+    for (int it = 0; it < n; ++it) {
+        const int st = it % kStages;
+        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
+        const Tile d = sm.tile[st];
+        if ((d.flags & kFirst) && ok) load_q(d.r, d.kvh);
+        const uint32_t kt = smem_u32(sm.ring[st]), vt = kt + kTileBytes;
+        const uint8_t *ktp = sm.ring[st], *vtp = ktp + kTileBytes;
+
+        // ---- S = Q K^T of this warp's tokens
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int blk = nt * 8 * ROWB;
+            if constexpr (kBf16) {
+                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kp = 0; kp < D / 32; ++kp) {
+                    uint32_t b[4];
+                    ldsm4(kt + ko[kp & 1] + blk + (kp >> 1) * 1024, b);
+                    mma_bf16(s0, qf[2 * kp], b[0], b[1]);
+                    mma_bf16(s1, qf[2 * kp + 1], b[2], b[3]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[nt][u] = (s0[u] + s1[u]) * s2;
+            } else {
+                // three tf32 products (the low parts' product, 2^-22 of the whole, is left out)
+                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f}, cr[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kp = 0; kp < D / 16; ++kp) {
+                    const float4 kx = *reinterpret_cast<const float4 *>(ktp + ko[kp & 1] + blk + (kp >> 1) * 1024);
+                    uint32_t h[4], w[4];
+                    split_tf32(kx.x, h[0], w[0]);
+                    split_tf32(kx.y, h[1], w[1]);
+                    split_tf32(kx.z, h[2], w[2]);
+                    split_tf32(kx.w, h[3], w[3]);
+                    mma_tf32(s0, qf[2 * kp], h[0], h[1]);
+                    mma_tf32(s1, qf[2 * kp + 1], h[2], h[3]);
+                    mma_tf32(cr, qf[2 * kp], w[0], w[1]);
+                    mma_tf32(cr, ql[2 * kp], h[0], h[1]);
+                    mma_tf32(cr, qf[2 * kp + 1], w[2], w[3]);
+                    mma_tf32(cr, ql[2 * kp + 1], h[2], h[3]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[nt][u] = with_correction(s0[u] + s1[u], cr[u]) * s2;
+            }
+        }
+        if (d.flags & kEdge) {
+            // tokens outside the row's range or on no page: no score, and a zero value row
+            auto hidden = [&](int t) {
+                const int pos = d.base + t;
+                return pos < d.lo || pos >= d.hi || ((sm.tile[st].bad[t >> 5] >> (t & 31)) & 1u);
+            };
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (hidden(tok0 + nt * 8 + tok_of(u & 1))) x[nt][u] = -INFINITY;
+            for (int i = tid; i < TT * CH; i += kMath) {
+                const int t = i / CH, ch = i % CH;         // (the order of a row's chunks does not matter)
+                if (hidden(t))
+                    *reinterpret_cast<uint4 *>(sm.ring[st] + kTileBytes + (t >> 3) * 8 * ROWB + (ch >> 3) * 1024 +
+                                               (t & 7) * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();      // before a later copy lands there
+        }
+        // ---- row maxima over the tile
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mx = max_nan(mx, max_nan(x[nt][2 * r], x[nt][2 * r + 1]));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            if (t4 == 0) sm.mx[warp][gq + 8 * r] = mx;
+        }
+        if (math_any(!ok)) break;          // a wait ran out: every warp leaves here
+        float corr[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float mx = m_run[r];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = max_nan(mx, sm.mx[w][gq + 8 * r]);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            corr[r] = ex2(m_run[r] - ref);
+            m_run[r] = mx;
+            float ls = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                const float p0 = ex2(x[nt][2 * r] - ref), p1 = ex2(x[nt][2 * r + 1] - ref);
+                ls += p0 + p1;
+                const int at = tok0 + nt * 8, h = gq + 8 * r;
                 if constexpr (kBf16) {
-                    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-                    const int row = tok0 + nt * 8 + (lane & 7);
-#pragma unroll
-                    for (int kp = 0; kp < D / 32; ++kp) {
-                        uint32_t b[4];
-                        ldsm4(smem_at(kt) + row * ROWB + (((4 * kp + (lane >> 3)) ^ (row & 7)) << 4), b);
-                        mma_bf16(s0, qf[2 * kp], b[0], b[1]);
-                        mma_bf16(s1, qf[2 * kp + 1], b[2], b[3]);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) x[nt][u] = s0[u] + s1[u];
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                    const float2 hf = __bfloat1622float2(hi);
+                    *reinterpret_cast<__nv_bfloat162 *>(&sm.p[0][h][at + 2 * t4]) = hi;
+                    *reinterpret_cast<__nv_bfloat162 *>(&sm.p[1][h][at + 2 * t4]) = __floats2bfloat162_rn(p0 - hf.x, p1 - hf.y);
                 } else {
-                    // three tf32 products (the low parts' product, 2^-22 of the whole, is left out)
-                    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f}, cr[4] = {0.f, 0.f, 0.f, 0.f};
-                    const int row = tok0 + nt * 8 + gq;
-#pragma unroll
-                    for (int kp = 0; kp < D / 16; ++kp) {
-                        const float4 kx = *reinterpret_cast<const float4 *>(
-                            kt + row * ROWB + (((4 * kp + t4) ^ ((row & 1) << 2)) << 4));
-                        uint32_t h[4], w[4];
-                        split_tf32(kx.x, h[0], w[0]);
-                        split_tf32(kx.y, h[1], w[1]);
-                        split_tf32(kx.z, h[2], w[2]);
-                        split_tf32(kx.w, h[3], w[3]);
-                        mma_tf32(s0, qf[2 * kp], h[0], h[1]);
-                        mma_tf32(s1, qf[2 * kp + 1], h[2], h[3]);
-                        mma_tf32(cr, qf[2 * kp], w[0], w[1]);
-                        mma_tf32(cr, ql[2 * kp], h[0], h[1]);
-                        mma_tf32(cr, qf[2 * kp + 1], w[2], w[3]);
-                        mma_tf32(cr, ql[2 * kp + 1], h[2], h[3]);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) x[nt][u] = with_correction(s0[u] + s1[u], cr[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const bool seen = off[tok0 + nt * 8 + 2 * t4 + (u & 1)] >= 0;
-                    x[nt][u] = seen ? x[nt][u] * s2 : -INFINITY;
+                    uint32_t hi, lo;
+                    split_tf32(p0, hi, lo);
+                    sm.p[0][h][at + t4] = __uint_as_float(hi);
+                    sm.p[1][h][at + t4] = __uint_as_float(lo);
+                    split_tf32(p1, hi, lo);
+                    sm.p[0][h][at + t4 + 4] = __uint_as_float(hi);
+                    sm.p[1][h][at + t4 + 4] = __uint_as_float(lo);
                 }
             }
-            // ---- row maxima over the tile
+            l_run[r] = l_run[r] * corr[r] + ls;
+        }
+        math_sync();
+        // ---- the tile's P V in accumulators of its own (the MMA truncates its sums: kept short), then into O.
+        // A non-finite value times a low part can be NaN where the product is infinite: such a tile is
+        // done again with the high parts alone.
+        float pv[NJ][4];
+        auto weigh = [&](bool low) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mx = max_nan(mx, max_nan(x[nt][2 * r], x[nt][2 * r + 1]));
-                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                if (t4 == 0) sm.mx[warp][gq + 8 * r] = mx;
-            }
-            __syncthreads();
-            float corr[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float mx = m_run[r];
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = max_nan(mx, sm.mx[w][gq + 8 * r]);
-                corr[r] = m_run[r] == mx ? 1.f : exp2f(m_run[r] - mx);
-                m_run[r] = mx;
-                float ls = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        p[u] = mx == -INFINITY ? 0.f : exp2f(x[nt][2 * r + u] - mx);
-                        ls += p[u];
-                    }
-                    const int at = tok0 + nt * 8 + 2 * t4;
-                    // weights keep 16 (bf16) or 22 (tf32) bits in two parts: one bf16 part alone would
-                    // cost half an ulp of the output
-                    if constexpr (kBf16) {
-                        const __nv_bfloat162 hi = __floats2bfloat162_rn(p[0], p[1]);
-                        const float2 hf = __bfloat1622float2(hi);
-                        *reinterpret_cast<__nv_bfloat162 *>(&sm.p[0][gq + 8 * r][at]) = hi;
-                        *reinterpret_cast<__nv_bfloat162 *>(&sm.p[1][gq + 8 * r][at]) =
-                            __floats2bfloat162_rn(p[0] - hf.x, p[1] - hf.y);
-                    } else {
-                        uint32_t h[2], w[2];
-                        split_tf32(p[0], h[0], w[0]);
-                        split_tf32(p[1], h[1], w[1]);
-                        *reinterpret_cast<uint2 *>(&sm.p[0][gq + 8 * r][at]) = make_uint2(h[0], h[1]);
-                        *reinterpret_cast<uint2 *>(&sm.p[1][gq + 8 * r][at]) = make_uint2(w[0], w[1]);
-                    }
-                }
-                l_run[r] = l_run[r] * corr[r] + ls;
-            }
-            __syncthreads();
-            // ---- the tile's P V in accumulators of its own (the MMA truncates its sums: kept short), then into O
-            float pv[NJ][4], pc[NJ][4];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) pv[j][u] = pc[j][u] = 0.f;
+            for (int j = 0; j < NJ; ++j) pv[j][0] = pv[j][1] = pv[j][2] = pv[j][3] = 0.f;
             if constexpr (kBf16) {
 #pragma unroll
                 for (int kp = 0; kp < TT / 16; ++kp) {
                     uint32_t ph[4], pl[4];
                     const int prow = lane & 15, pcol = kp * 16 + (lane >> 4) * 8;
-                    ldsm4(smem_at(&sm.p[0][prow][pcol]), ph);
-                    ldsm4(smem_at(&sm.p[1][prow][pcol]), pl);
-                    const int row = kp * 16 + (lane & 15);
+                    ldsm4(smem_u32(&sm.p[0][prow][pcol]), ph);
+                    if (low) ldsm4(smem_u32(&sm.p[1][prow][pcol]), pl);
 #pragma unroll
                     for (int jp = 0; jp < NJ / 2; ++jp) {
                         uint32_t b[4];
-                        const int ch = warp * (D / 32) + 2 * jp + (lane >> 4);
-                        ldsm4t(smem_at(vt) + row * ROWB + ((ch ^ (row & 7)) << 4), b);
+                        ldsm4t(vt + vo[jp] + kp * 16 * ROWB, b);
                         mma_bf16(pv[2 * jp], ph, b[0], b[1]);
                         mma_bf16(pv[2 * jp + 1], ph, b[2], b[3]);
-                        mma_bf16(pc[2 * jp], pl, b[0], b[1]);
-                        mma_bf16(pc[2 * jp + 1], pl, b[2], b[3]);
+                        if (low) {
+                            mma_bf16(pv[2 * jp], pl, b[0], b[1]);
+                            mma_bf16(pv[2 * jp + 1], pl, b[2], b[3]);
+                        }
                     }
                 }
             } else {
 #pragma unroll
                 for (int kp = 0; kp < TT / 8; ++kp) {
+                    // k slots t4 and t4 + 4 are tokens 2 t4 and 2 t4 + 1
                     uint32_t ph[4], pl[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int prow = gq + 8 * (u & 1), pcol = kp * 8 + t4 + 4 * (u >> 1);
-                        ph[u] = __float_as_uint(sm.p[0][prow][pcol]);
-                        pl[u] = __float_as_uint(sm.p[1][prow][pcol]);
+                    for (int u = 0; u < 2; ++u) {
+                        const float2 h = *reinterpret_cast<const float2 *>(&sm.p[0][gq + 8 * u][kp * 8 + 2 * t4]);
+                        ph[u] = __float_as_uint(h.x);
+                        ph[2 + u] = __float_as_uint(h.y);
+                        if (low) {
+                            const float2 l = *reinterpret_cast<const float2 *>(&sm.p[1][gq + 8 * u][kp * 8 + 2 * t4]);
+                            pl[u] = __float_as_uint(l.x);
+                            pl[2 + u] = __float_as_uint(l.y);
+                        }
                     }
                     // NJ coordinates in a row per lane: column gq of each of the NJ column blocks
                     float v0[NJ], v1[NJ];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = kp * 8 + t4 + 4 * e;
-                        const int byte = (warp * (D / 4) + gq * NJ) * 4;
-                        const uint8_t *src = vt + row * ROWB + (((byte >> 4) ^ ((row & 3) << 1)) << 4) + (byte & 15);
-                        float *dst = e ? v1 : v0;
-                        if constexpr (NJ == 4) *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src);
-                        else *reinterpret_cast<float2 *>(dst) = *reinterpret_cast<const float2 *>(src);
+                    if constexpr (NJ == 4) {
+                        *reinterpret_cast<float4 *>(v0) = *reinterpret_cast<const float4 *>(vtp + vo[0] + kp * 8 * ROWB);
+                        *reinterpret_cast<float4 *>(v1) = *reinterpret_cast<const float4 *>(vtp + vo[1] + kp * 8 * ROWB);
+                    } else {
+                        *reinterpret_cast<float2 *>(v0) = *reinterpret_cast<const float2 *>(vtp + vo[0] + kp * 8 * ROWB);
+                        *reinterpret_cast<float2 *>(v1) = *reinterpret_cast<const float2 *>(vtp + vo[1] + kp * 8 * ROWB);
                     }
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) {
-                        uint32_t h0, h1, w0_, w1_;
-                        split_tf32(v0[j], h0, w0_);
-                        split_tf32(v1[j], h1, w1_);
+                        uint32_t h0, h1, l0, l1;
+                        split_tf32(v0[j], h0, l0);
+                        split_tf32(v1[j], h1, l1);
                         mma_tf32(pv[j], ph, h0, h1);
-                        mma_tf32(pc[j], ph, w0_, w1_);
-                        mma_tf32(pc[j], pl, h0, h1);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) o[j][u] = fmaf(o[j][u], corr[u >> 1], with_correction(pv[j][u], pc[j][u]));
-
-            if (!(d.flags & kLast)) continue;
-            // ---- the end of this CTA's piece of the group: the sums of the warps
-            float L[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float l = l_run[r];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if (t4 == 0) sm.sum[warp][gq + 8 * r] = l;
-            }
-            __syncthreads();
-            const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
-            float *part = nullptr;
-            if (!(d.flags & kWhole)) {
-                // slot 2c holds the piece that begins with CTA c's part, slot 2c + 1 the other
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (d.g0 > w0 ? 1 : 0);
-                part = parts + slot * piece_floats(a.G, D);
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                L[r] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) L[r] += sm.sum[w][gq + 8 * r];
-                const int h = gq + 8 * r;
-                if (h < a.G) {
-                    if (part) {
-                        if (warp == 0 && t4 == 0) {
-                            part[2 * h] = m_run[r];
-                            part[2 * h + 1] = L[r];
-                        }
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) part[piece_ml(a.G) + h * D + dim_of(j, c)] = o[j][2 * r + c];
-                    } else {
-                        T *out = static_cast<T *>(a.out) + (head + h) * D;
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                out[dim_of(j, c)] = from_f32<T>(L[r] == 0.f ? 0.f : o[j][2 * r + c] / L[r]);
-                        if (a.lse && warp == 0 && t4 == 0)
-                            a.lse[head + h] = L[r] == 0.f ? -INFINITY : (m_run[r] + log2f(L[r])) * kLn2;
-                    }
-                }
-                m_run[r] = -INFINITY;
-                l_run[r] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-            if (!part) continue;
-
-            // ---- the last piece to arrive joins them all
-            const int c_first = (int)(((d.g0 + 1) * P - 1) / W), c_last = (int)(((d.g0 + d.len) * P - 1) / W);
-            const int pieces = c_last - c_first + 1;
-            __threadfence();
-            __syncthreads();
-            int32_t *counter = arrived + (int64_t)d.r * a.Hkv + d.kvh;
-            if (tid == 0) sm.last = atomicAdd(counter, 1) == pieces - 1;
-            __syncthreads();
-            if (!sm.last) continue;
-            __threadfence();
-            if (tid == 0) *counter = 0;
-            auto piece = [&](int i) {
-                const int c = c_first + i;
-                const bool second = i == 0 && W * c / P < d.g0;
-                return parts + (2 * (int64_t)c + (second ? 1 : 0)) * piece_floats(a.G, D);
-            };
-            const int jh = tid & 15, ji = tid >> 4;        // this thread's head and first piece of the statistics
-            float M = -INFINITY;
-            if (jh < a.G)
-                for (int i = ji; i < pieces; i += kThreads / 16) M = max_nan(M, __ldcg(piece(i) + 2 * jh));
-            sm.mx[ji][jh] = M;
-            __syncthreads();
-            M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kThreads / 16; ++w) M = max_nan(M, sm.mx[w][jh]);
-            constexpr int ITEMS = kRows * D / 4 / kThreads;
-            float4 acc[ITEMS];
-#pragma unroll
-            for (int e = 0; e < ITEMS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            float Ls = 0.f;
-            for (int base = 0; base < pieces; base += kJoin) {
-                const int cnt = min(kJoin, pieces - base);
-                __syncthreads();
-                if (jh < a.G)
-                    for (int i = ji; i < cnt; i += kThreads / 16) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(piece(base + i)) + jh);
-                        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-                        sm.weight[i][jh] = f;
-                        Ls += f == 0.f ? 0.f : ml.y * f;
-                    }
-                __syncthreads();
-#pragma unroll
-                for (int e = 0; e < ITEMS; ++e) {
-                    const int at = tid + e * kThreads, h = at / (D / 4);
-                    if (h < a.G) {
-#pragma unroll 8
-                        for (int i = 0; i < cnt; ++i) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(base + i) + piece_ml(a.G)) + at);
-                            const float f = sm.weight[i][h];
-                            acc[e].x = fmaf(v.x, f, acc[e].x);
-                            acc[e].y = fmaf(v.y, f, acc[e].y);
-                            acc[e].z = fmaf(v.z, f, acc[e].z);
-                            acc[e].w = fmaf(v.w, f, acc[e].w);
+                        if (low) {
+                            mma_tf32(pv[j], ph, l0, l1);
+                            mma_tf32(pv[j], pl, h0, h1);
                         }
                     }
                 }
             }
-            sm.sum[ji][jh] = Ls;
-            __syncthreads();
-            auto total = [&](int h) {
-                float s = 0.f;
+        };
+        weigh(true);
+        float odd = 0.f;                   // stays 0 if everything is finite
 #pragma unroll
-                for (int w = 0; w < kThreads / 16; ++w) s += sm.sum[w][h];
-                return s;
-            };
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int e = 0; e < ITEMS; ++e) {
-                const int at = tid + e * kThreads, h = at / (D / 4);
-                if (h < a.G) {
-                    const float l = total(h), v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
-                    float y[4];
+            for (int u = 0; u < 4; ++u) odd = fmaf(pv[j][u], 0.f, odd);
+        if (__any_sync(0xffffffffu, odd != 0.f)) weigh(false);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) y[c] = l == 0.f ? 0.f : v[c] / l;
-                    store_vec<4>(static_cast<T *>(a.out) + head * D + (int64_t)at * 4, y);
-                }
-            }
-            if (a.lse && ji == 0 && jh < a.G) {
-                const float l = total(jh);
-                a.lse[head + jh] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
-            }
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[j][u] = fmaf(o[j][u], corr[u >> 1], pv[j][u]);
+
+        if (!(d.flags & kLast)) continue;
+        // ---- the end of this CTA's piece of the group: the sums of the warps
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float l = l_run[r];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if (t4 == 0) sm.sum[warp][gq + 8 * r] = l;
         }
-        cp_wait<0>();
+        math_sync();
+        const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
+        float *part = nullptr;
+        if (!(d.flags & kWhole))           // slot 2c: the piece that begins with CTA c's part; 2c + 1: its other one
+            part = parts + (2 * (int64_t)blockIdx.x + (d.g0 > w0 ? 1 : 0)) * piece_floats(a.G, D);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) L += sm.sum[w][gq + 8 * r];
+            const int h = gq + 8 * r;
+            if (h < a.G) {
+                if (part) {
+                    if (warp == 0 && t4 == 0) reinterpret_cast<float2 *>(part)[h] = make_float2(m_run[r], L);
+                } else if (a.lse && warp == 0 && t4 == 0) {
+                    a.lse[head + h] = L == 0.f ? -INFINITY : (m_run[r] + log2f(L)) * kLn2;
+                }
+                const float inv = part ? 1.f : L == 0.f ? 0.f : 1.f / L;
+                // a lane's coordinates come in runs of 2 (bf16) or NJ (fp32)
+                constexpr int RUN = kBf16 ? 2 : NJ, RUNS = 2 * NJ / RUN;
+#pragma unroll
+                for (int e = 0; e < RUNS; ++e) {
+                    float y[RUN];
+#pragma unroll
+                    for (int c = 0; c < RUN; ++c) y[c] = (kBf16 ? o[e][2 * r + c] : o[c][2 * r + e]) * inv;
+                    const int at = h * D + (kBf16 ? dim_of(e, 0) : dim_of(0, e));
+                    if (part) store_vec<RUN>(part + piece_ml(a.G) + at, y);
+                    else store_vec<RUN>(static_cast<T *>(a.out) + head * D + at, y);
+                }
+            }
+            m_run[r] = -INFINITY;
+            l_run[r] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        if (!part) continue;
+
+        // ---- the last piece to arrive joins them all; with many pieces the last of a set of about sqrt(pieces)
+        // joins the set into its first piece's place, and the last set to arrive joins the sets
+        const int c_first = (int)(((d.g0 + 1) * P - 1) / W), c_last = (int)(((d.g0 + d.len) * P - 1) / W);
+        const int pieces = c_last - c_first + 1, mine_i = (int)blockIdx.x - c_first;
+        const int slot0 = 2 * c_first + (W * c_first / P < d.g0 ? 1 : 0);
+        auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (c_first + i); };
+        int set = pieces;
+        if (pieces > kDirect) {
+            set = kDirect / 2;
+            while (set * set < pieces) ++set;
+        }
+        const int i0 = mine_i / set * set, in_set = min(set, pieces - i0), sets = (pieces + set - 1) / set;
+        if (!arrive(arrived + slot(i0), in_set)) continue;
+        if (sets == 1) {
+            join(pieces, slot, head, nullptr);
+        } else {
+            join(in_set, [&](int i) { return slot(i0 + i); }, head, parts + (int64_t)slot(i0) * piece_floats(a.G, D));
+            if (arrive(arrived + 2 * kMaxWorkers + slot0, sets))
+                join(sets, [&](int i) { return slot(i * set); }, head, nullptr);
+        }
+        math_sync();                       // shared memory of the join before the next tile's
     }
     // ---- rows that attend nothing
     for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const RowSpan s = row_span(a, r);
         if (s.seq < 0 || s.hi > s.lo) continue;
         T *out = static_cast<T *>(a.out) + (int64_t)r * a.Hq * D;
-        for (int i = tid; i < a.Hq * D; i += kThreads) out[i] = from_f32<T>(0.f);
+        for (int i = tid; i < a.Hq * D; i += kMath) out[i] = from_f32<T>(0.f);
         if (a.lse)
-            for (int i = tid; i < a.Hq; i += kThreads) a.lse[(int64_t)r * a.Hq + i] = -INFINITY;
+            for (int i = tid; i < a.Hq; i += kMath) a.lse[(int64_t)r * a.Hq + i] = -INFINITY;
     }
     // no early trigger: a kernel behind this one may read `out` before its own wait
 }
 
+// The pool as [rows / 8][D * sizeof(T) / 128][8][128 bytes]: a box is `box` rows in the ring's layout.
 template <typename T, int D>
+bool pool_map(CUtensorMap *map, const void *pool, const PagedAttnArgs &a, int box) {
+    constexpr int ROWB = D * (int)sizeof(T), E = 128 / (int)sizeof(T);
+    const uint64_t rows = ((uint64_t)a.n_pages << a.lps) * a.Hkv;
+    const cuuint64_t dims[4] = {(cuuint64_t)E, 8, ROWB / 128, rows / 8};
+    const cuuint64_t strides[3] = {ROWB, 128, 8 * ROWB};
+    const cuuint32_t boxd[4] = {(cuuint32_t)E, 8, ROWB / 128, (cuuint32_t)(box / 8)};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return tensor_map_encoder()(map, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                                const_cast<void *>(pool), dims, strides, boxd, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool kTma>
 cudaError_t launch(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaStream_t st) {
     const size_t smem = sizeof(Shared<T, D>);
+    static_assert(2 * (sizeof(Shared<T, D>) + 1024) <= 228 * 1024, "two CTAs per SM");
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
+    CUtensorMap kmap{}, vmap{};
+    if (kTma) {
+        const int box = (1 << a.lps) < kBox ? 1 << a.lps : kBox;
+        if (!tensor_map_encoder() || !pool_map<T, D>(&kmap, a.kpool, a, box) || !pool_map<T, D>(&vmap, a.vpool, a, box))
+            return cudaErrorNotSupported;
+    }
     // no more CTAs than the longest possible rows would keep busy
-    const int64_t longest = min64((int64_t)a.max_pages << a.lps, a.window > 0 ? a.window : INT64_MAX);
+    const int64_t longest = min64((int64_t)a.max_pages << a.lps, a.window > 0 ? (int64_t)a.window + kBox : INT64_MAX);
     const int64_t tiles = (longest + Shared<T, D>::TT - 1) / Shared<T, D>::TT * a.Hkv * a.rows;
     const int grid = (int)max64(1, min64(kMaxWorkers, (tiles + kMinTiles - 1) / kMinTiles));
     ProfScope ps("paged_decode", st);
-    return launch_pdl(paged_attn_kernel<T, D>, dim3(grid), dim3(kThreads), smem, st, a, parts, arrived);
+    return launch_pdl(paged_attn_kernel<T, D, kTma>, dim3(grid), dim3(kThreads), smem, st, a, kmap, vmap, parts, arrived);
+}
+
+// Pages of 8 rows and more are copied by TMA, whose boxes are whole blocks of 8 rows; smaller ones row by row.
+template <typename T, int D>
+cudaError_t launch_page(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaStream_t st) {
+    return a.lps >= 3 ? launch<T, D, true>(a, parts, arrived, st) : launch<T, D, false>(a, parts, arrived, st);
 }
 
 size_t pieces_bytes(const PagedAttnArgs &a) { return (size_t)kMaxWorkers * 2 * piece_floats(a.G, a.d) * sizeof(float); }
 
 }  // namespace
 
-// Two pieces per CTA, then the arrival counters of the groups (behind the
-// part whose size is the configuration's alone: a call of fewer rows finds
-// its counters where one of more rows does).
-size_t paged_attn_workspace(const PagedAttnArgs &a) { return pieces_bytes(a) + (size_t)a.rows * a.Hkv * sizeof(int32_t); }
+// Two pieces per CTA, then a counter per piece for sets and one for groups.
+size_t paged_attn_workspace(const PagedAttnArgs &a) { return pieces_bytes(a) + 4 * kMaxWorkers * sizeof(int32_t); }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, cudaStream_t st) {
     float *parts = static_cast<float *>(a.ws);
     int32_t *arrived = reinterpret_cast<int32_t *>(static_cast<char *>(a.ws) + pieces_bytes(a));
     if (a.dtype == ZHA_BF16)
-        return a.d == 128 ? launch<__nv_bfloat16, 128>(a, parts, arrived, st)
-                          : launch<__nv_bfloat16, 64>(a, parts, arrived, st);
-    return a.d == 128 ? launch<float, 128>(a, parts, arrived, st) : launch<float, 64>(a, parts, arrived, st);
+        return a.d == 128 ? launch_page<__nv_bfloat16, 128>(a, parts, arrived, st)
+                          : launch_page<__nv_bfloat16, 64>(a, parts, arrived, st);
+    return a.d == 128 ? launch_page<float, 128>(a, parts, arrived, st) : launch_page<float, 64>(a, parts, arrived, st);
 }
 
 }  // namespace zha
