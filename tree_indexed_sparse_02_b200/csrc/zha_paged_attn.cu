@@ -138,6 +138,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division takes hundreds of cycles)
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A piece of a group in the workspace: (m, l) of its G heads, padded to whole
 // float4s, then o as [G][D].
 __host__ __device__ __forceinline__ int piece_ml(int G) { return (2 * G + 3) & ~3; }
@@ -169,17 +174,95 @@ struct Shared {
         alignas(16) PT p[2][kRows][PS];
         float weight[kSetMax][kRows];
     };
+    static constexpr int QROW = D * (int)sizeof(T) + 16;           // padded: no bank twice
+    static constexpr int QS = sizeof(T) == 2 ? 2 : 1;              // places for the queries of a piece
+    alignas(16) uint8_t q[QS][kRows][QROW];
     Tile tile[kStages];
     float mx[2 * kWarps][kRows], sum[2 * kWarps][kRows];
     int64_t scan[kThreads / 32];
     int64_t start_before;
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages], q_empty[QS];
     int start_row, last, abort;
 };
 
+// Joins cnt pieces in slots s0, s1, s1 + step, ... of the workspace: all heads' statistics, then o. The
+// result goes to the group's output, or back into slot s0.
+template <typename T, int D>
+__device__ __forceinline__ void join(const PagedAttnArgs &a, float *parts, Shared<T, D> &sm, int cnt, int s0, int s1, int step,
+                              int64_t head, bool back) {
+    const int tid = threadIdx.x;
+    auto piece = [&](int i) { return parts + (int64_t)(i == 0 ? s0 : s1 + (i - 1) * step) * piece_floats(a.G, D); };
+    float *to = back ? piece(0) : nullptr;
+    constexpr int FLY = 8;             // loads in flight
+    const int items = a.G * (D / 4);
+    const int jh = tid & 15, ji = tid >> 4;
+    float2 ml[kSetMax / 8];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int e = 0; e < kSetMax / 8; ++e) {
+        const int i = ji + 8 * e;
+        ml[e] = i < cnt && jh < a.G ? __ldcg(reinterpret_cast<const float2 *>(piece(i)) + jh) : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int e = 0; e < kSetMax / 8; ++e) M = max_nan(M, ml[e].x);
+    sm.mx[ji][jh] = M;
+    math_sync();
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = max_nan(M, sm.mx[w][jh]);
+#pragma unroll
+    for (int e = 0; e < kSetMax / 8; ++e) {
+        const float f = ml[e].x == -INFINITY ? 0.f : ex2(ml[e].x - M);
+        sm.weight[ji + 8 * e][jh] = f;
+        L += f == 0.f ? 0.f : ml[e].y * f;
+    }
+    sm.sum[ji][jh] = L;
+    math_sync();
+    auto total = [&](int h) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += sm.sum[w][h];
+        return s;
+    };
+    // small code on purpose: it runs once or twice in a CTA's life, from a cold instruction cache
+#pragma unroll 1
+    for (int at = tid; at < items; at += kMath) {
+        const int h = at / (D / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i0 = 0; i0 < cnt; i0 += FLY) {
+            float4 v[FLY];
+#pragma unroll
+            for (int u = 0; u < FLY; ++u)
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(piece(min(i0 + u, cnt - 1)) + piece_ml(a.G)) + at);
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) {
+                const float f = i0 + u < cnt ? sm.weight[i0 + u][h] : 0.f;
+                if (f == 0.f) continue;    // a piece without weight may hold anything
+                acc.x = fmaf(v[u].x, f, acc.x);
+                acc.y = fmaf(v[u].y, f, acc.y);
+                acc.z = fmaf(v[u].z, f, acc.z);
+                acc.w = fmaf(v[u].w, f, acc.w);
+            }
+        }
+        if (to) {                          // over piece 0, whose quarter of a row only this thread reads
+            reinterpret_cast<float4 *>(to + piece_ml(a.G))[at] = acc;
+        } else {
+            const float inv = 1.f / total(h), y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            store_vec<4>(static_cast<T *>(a.out) + head * D + (int64_t)at * 4, total(h) == 0.f ? zero : y);
+        }
+    }
+    if (ji == 0 && jh < a.G) {
+        const float l = total(jh);
+        if (to) reinterpret_cast<float2 *>(to)[jh] = make_float2(M, l);
+        else if (a.lse) a.lse[head + jh] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+}
+
 template <typename T, int D, bool kTma>
 __global__ void __launch_bounds__(kThreads, 2)
-paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   float *parts, int32_t *arrived) {
     using S = Shared<T, D>;
     constexpr bool kBf16 = sizeof(T) == 2;
@@ -197,16 +280,24 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
             mbar_init(smem_u32(&sm.full[i]), kTma ? 1 : 33);
             mbar_init(smem_u32(&sm.empty[i]), kWarps);
         }
+        for (int i = 0; i < S::QS; ++i) mbar_init(smem_u32(&sm.q_empty[i]), kWarps);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         fence_proxy_async_smem();
+        if (kTma) {
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+        }
     }
+    __syncthreads();
     pdl_wait();
 
-    // ---- this CTA's part [w0, w1) of the list of all tiles, and the row it begins in
-    const int per = (a.rows + kThreads - 1) / kThreads;
-    const int ra = min(tid * per, a.rows), rb = min(ra + per, a.rows);
+    // ---- this CTA's part [w0, w1) of the list of all tiles, and the row it begins in: prefix sums over the
+    // rows, by every warp for itself where a warp holds them all
     auto tiles_of = [&](const RowSpan &s) { return s.hi > s.lo ? (s.hi - (s.lo & -box) + TT - 1) / TT : 0; };
+    const bool few = a.rows <= 32;
+    const int per = few ? 1 : (a.rows + kThreads - 1) / kThreads;
+    const int ra = min((few ? lane : tid) * per, a.rows), rb = min(ra + per, a.rows);
     int64_t mine = 0;
     for (int r = ra; r < rb; ++r) mine += tiles_of(row_span(a, r));
     int64_t incl = mine;
@@ -215,21 +306,25 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
         const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    if (lane == 31) sm.scan[warp] = incl;
-    __syncthreads();
     int64_t before = incl - mine, all = 0;
+    if (few) {
+        all = __shfl_sync(0xffffffffu, incl, 31);
+    } else {
+        if (lane == 31) sm.scan[warp] = incl;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sm.scan[w];
-        all += sm.scan[w];
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sm.scan[w];
+            all += sm.scan[w];
+        }
     }
     const int64_t W = all * a.Hkv;
     const int64_t want = (W + kMinTiles - 1) / kMinTiles;
     const int P = want < gridDim.x ? (int)want : (int)gridDim.x;    // CTAs that get a part
-    const int64_t w0 = (int)blockIdx.x < P ? W * blockIdx.x / P : 0;
-    const int64_t w1 = (int)blockIdx.x < P ? W * (blockIdx.x + 1) / P : 0;
+    const int64_t w0 = (int)blockIdx.x < P ? quot(W * blockIdx.x, P) : 0;
+    const int64_t w1 = (int)blockIdx.x < P ? quot(W * (blockIdx.x + 1), P) : 0;
     const int n = (int)(w1 - w0);
-    if (n > 0 && w0 >= before * a.Hkv && w0 < (before + mine) * a.Hkv) {
+    if (n > 0 && (!few || warp == kWarps) && w0 >= before * a.Hkv && w0 < (before + mine) * a.Hkv) {
         int64_t at = before;
         for (int r = ra; r < rb; ++r) {
             const int t = tiles_of(row_span(a, r));
@@ -241,59 +336,96 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
             at += t;
         }
     }
-    __syncthreads();
+    if (few) __syncwarp();
+    else __syncthreads();
 
     if (warp == kWarps) {
         // ================= the copying warp
         if (n == 0) return;
-        int c_r = sm.start_row;
-        RowSpan span = row_span(a, c_r);
-        int c_len = tiles_of(span);
-        int64_t c_g0 = sm.start_before * a.Hkv;
-        int c_kvh = (int)((w0 - c_g0) / c_len);
-        c_g0 += (int64_t)c_kvh * c_len;
-        int c_i = (int)(w0 - c_g0);
-        // a lane's pages: its box of the tile (TMA), or its tokens lane, lane + 32, ... (small pages)
+        // where a walk over the list stands: tile i of the group (r, kvh), whose len tiles begin at g0
+        struct Walk {
+            int r, kvh, i, len;
+            int64_t g0;
+            RowSpan span;
+        };
+        Walk next;
+        next.r = sm.start_row;
+        next.span = row_span(a, next.r);
+        next.len = tiles_of(next.span);
+        next.g0 = sm.start_before * a.Hkv;
+        next.kvh = (int)quot(w0 - next.g0, next.len);
+        next.g0 += (int64_t)next.kvh * next.len;
+        next.i = (int)(w0 - next.g0);
+        // A lane looks up one box's page of one of the next `batch` tiles of a group (TMA), or the pages of
+        // the tokens lane, lane + 32, ... of the next tile (small pages), a batch ahead of the copies.
         constexpr int NP = kTma ? 1 : TT / 32;
-        const int boxes = TT / box;
-        const int lbox = 31 - __clz(box);
-        int page[NP];
-        auto token = [&](int i) { return (span.lo & -box) + c_i * TT + (kTma ? lane * box : lane + 32 * i); };
+        const int lbox = 31 - __clz(box), boxes = kTma ? TT >> lbox : 1, lboxes = 31 - __clz(boxes);
+        const int batch = kTma ? 32 >> lboxes : 1;
+        const int lt = kTma ? lane >> lboxes : 0, lb = kTma ? lane & (boxes - 1) : 0;
+        int page[NP], page_next[NP];
+        auto token = [&](const Walk &c, int i) {
+            return (c.span.lo & -box) + (c.i + lt) * TT + (kTma ? lb * box : lane + 32 * i);
+        };
         auto look = [&]() {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int pos = token(i);
-                page[i] = (!kTma || lane < boxes) && pos < span.hi
-                              ? __ldg(a.table + (int64_t)span.seq * a.max_pages + (pos >> a.lps)) : -1;
+                const int pos = token(next, i);
+                page_next[i] = next.i + lt < next.len && pos < next.span.hi
+                                   ? __ldg(a.table + (int64_t)next.span.seq * a.max_pages + (pos >> a.lps)) : -1;
             }
         };
         look();
-        int k = 0;
-        for (; k < n; ++k) {
-            const int st = k % kStages;
+        int k = 0, seg = -1;               // tiles issued, pieces begun
+        Walk c = next;
+        int left = 0, off = 0;             // tiles left of the batch, and the next one's place in it
+        for (; k < n; ++k, --left, ++off) {
+            if (left == 0) {
+                c = next;
+                off = 0;
+                left = min(batch, c.len - c.i);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) page[i] = page_next[i];
+                if (k + left < n) {
+                    next.i += left;
+                    if (next.i == next.len) {
+                        next.i = 0;
+                        next.g0 += next.len;
+                        if (++next.kvh == a.Hkv) {
+                            next.kvh = 0;
+                            do {
+                                next.span = row_span(a, ++next.r);
+                                next.len = tiles_of(next.span);
+                            } while (next.len == 0);
+                        }
+                    }
+                    look();
+                }
+            }
+            const int st = k % kStages, ci = c.i + off;
             Tile d;
-            d.r = c_r;
-            d.kvh = c_kvh;
-            d.len = c_len;
-            d.g0 = c_g0;
-            d.base = (span.lo & -box) + c_i * TT;
-            d.lo = span.lo;
-            d.hi = span.hi;
-            d.flags = ((k == 0 || c_i == 0) ? kFirst : 0) | ((k == n - 1 || c_i == c_len - 1) ? kLast : 0) |
-                      ((c_g0 >= w0 && c_g0 + c_len <= w1) ? kWhole : 0) |
+            d.r = c.r;
+            d.kvh = c.kvh;
+            d.len = c.len;
+            d.g0 = c.g0;
+            d.base = (c.span.lo & -box) + ci * TT;
+            d.lo = c.span.lo;
+            d.hi = c.span.hi;
+            d.flags = ((k == 0 || ci == 0) ? kFirst : 0) | ((k == n - 1 || ci == c.len - 1) ? kLast : 0) |
+                      ((c.g0 >= w0 && c.g0 + c.len <= w1) ? kWhole : 0) |
                       ((d.base < d.lo || d.base + TT > d.hi) ? kEdge : 0);
             d.bad[0] = d.bad[1] = d.bad[2] = d.bad[3] = 0;
             int64_t row[NP];               // first row of the copy in its pool, -1: none
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int pos = token(i);
-                const bool in = (!kTma || lane < boxes) && pos < span.hi, ok = in && (unsigned)page[i] < (unsigned)a.n_pages;
-                row[i] = ok ? (((int64_t)page[i] * a.Hkv + c_kvh) << a.lps) + (pos & ((1 << a.lps) - 1)) : -1;
-                const uint32_t bad = __ballot_sync(0xffffffffu, in && !ok);
+                const int pos = token(c, i);
+                const bool in = (!kTma || lt == off) && pos < c.span.hi, ok = in && (unsigned)page[i] < (unsigned)a.n_pages;
+                row[i] = ok ? (((int64_t)page[i] * a.Hkv + c.kvh) << a.lps) + (pos & ((1 << a.lps) - 1)) : -1;
+                uint32_t bad = __ballot_sync(0xffffffffu, in && !ok);
                 if (bad) {
                     if (in && !ok) set_status(a.status, ZHA_ERR_INVALID_ARG);
                     d.flags |= kEdge;
                     if constexpr (kTma) {
+                        bad >>= off << lboxes;     // one bit a box
 #pragma unroll
                         for (int w = 0; w < (TT + 31) / 32; ++w)
                             for (int t = 0; t < 32; ++t)
@@ -303,33 +435,26 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
                     }
                 }
             }
-            // the next tile's pages are on their way while this one waits for its place
-            if (++c_i == c_len && k + 1 < n) {
-                c_i = 0;
-                c_g0 += c_len;
-                if (++c_kvh == a.Hkv) {
-                    c_kvh = 0;
-                    do {
-                        span = row_span(a, ++c_r);
-                        c_len = tiles_of(span);
-                    } while (c_len == 0);
-                }
-            }
-            if (k + 1 < n) look();
             if (k >= kStages && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.empty[st]), (k / kStages - 1) & 1,
                                                                            kWaitCycles, abort, a.status)))
+                break;
+            const bool first = d.flags & kFirst;
+            seg += first;
+            // a piece's queries come with its first tile, once the warps hold those that were in their place
+            if (first && seg >= S::QS && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.q_empty[seg % S::QS]),
+                                                                                    (seg / S::QS - 1) & 1, kWaitCycles, abort, a.status)))
                 break;
             const uint32_t kb = smem_u32(sm.ring[st]), vb = kb + kTileBytes, full = smem_u32(&sm.full[st]);
             if (lane == 0) sm.tile[st] = d;
             if constexpr (kTma) {
                 const bool ok = row[0] >= 0;
                 const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
-                if (lane == 0) mbar_expect_tx(full, cnt * 2u * (uint32_t)box * ROWB);
+                if (lane == 0) mbar_expect_tx(full, cnt * 2u * (uint32_t)box * ROWB + (first ? a.G * ROWB : 0));
                 __syncwarp();
                 if (ok) {
-                    const uint32_t off = (uint32_t)lane * box * ROWB;
-                    tma_load_4d(kb + off, &kmap, (int)(row[0] >> 3), full);
-                    tma_load_4d(vb + off, &vmap, (int)(row[0] >> 3), full);
+                    const uint32_t at = (uint32_t)lb * box * ROWB;
+                    tma_load_4d(kb + at, &kmap, (int)(row[0] >> 3), full);
+                    tma_load_4d(vb + at, &vmap, (int)(row[0] >> 3), full);
                 }
             } else {
 #pragma unroll 4
@@ -344,14 +469,18 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
                     }
                     const bool ok = r2 >= 0;
                     const int64_t at = (ok ? r2 : 0) * ROWB + ch * 16;
-                    const uint32_t off = (tok >> 3) * 8 * ROWB + (ch >> 3) * 1024 + (tok & 7) * 128 + (((ch & 7) ^ (tok & 7)) << 4);
-                    cp16(kb + off, static_cast<const char *>(a.kpool) + at, ok);
-                    cp16(vb + off, static_cast<const char *>(a.vpool) + at, ok);
+                    const uint32_t to = (tok >> 3) * 8 * ROWB + (ch >> 3) * 1024 + (tok & 7) * 128 + (((ch & 7) ^ (tok & 7)) << 4);
+                    cp16(kb + to, static_cast<const char *>(a.kpool) + at, ok);
+                    cp16(vb + to, static_cast<const char *>(a.vpool) + at, ok);
                 }
                 cp_arrive(full);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                if (lane == 0) mbar_expect_tx(full, first ? a.G * ROWB : 0);
+                __syncwarp();
             }
+            if (first && lane < a.G)
+                bulk_load(smem_u32(sm.q[seg % S::QS][lane]), static_cast<const T *>(a.q) + ((int64_t)d.r * a.Hq + d.kvh * a.G + lane) * D,
+                          ROWB, full);
         }
         // given up: the copies in flight still land before the CTA may end
         if (k < n)
@@ -362,23 +491,22 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
 
     // ================= the computing warps
     const int gq = lane >> 2, t4 = lane & 3;
-    // Q fragments: bf16 as they are; fp32 split in two tf32 parts
+    // Q fragments (fp32 is split in two tf32 parts where it is used: both parts of all would not fit the registers)
     constexpr int KS = kBf16 ? D / 16 : D / 8;
-    uint32_t qf[KS][4], ql[kBf16 ? 1 : KS][4];
+    uint32_t qf[KS][4];
     float o[NJ][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     const float s2 = a.s * kLog2e;
     const int tok0 = warp * (TT / 4);
 
-    auto load_q = [&](int r, int kvh) {
-        const T *q = static_cast<const T *>(a.q) + ((int64_t)r * a.Hq + kvh * a.G) * D;
+    auto load_q = [&](int place) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int h = gq + 8 * half;
             const bool ok = h < a.G;
             if constexpr (kBf16) {
-                const uint32_t *row = reinterpret_cast<const uint32_t *>(q + (ok ? h : 0) * D);
+                const uint32_t *row = reinterpret_cast<const uint32_t *>(sm.q[place][h]);
 #pragma unroll
                 for (int st = 0; st < KS; ++st) {
                     qf[st][half] = ok ? row[st * 8 + t4] : 0u;
@@ -386,14 +514,14 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
                 }
             } else {
                 // coordinates of 16 are dealt to the k slots so that a lane's are 4 in a row
-                const float4 *row = reinterpret_cast<const float4 *>(q + (ok ? h : 0) * D);
+                const float4 *row = reinterpret_cast<const float4 *>(sm.q[place][h]);
 #pragma unroll
                 for (int st = 0; st < KS; st += 2) {
                     const float4 x = ok ? row[st * 2 + t4] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    split_tf32(x.x, qf[st][half], ql[st][half]);
-                    split_tf32(x.y, qf[st][2 + half], ql[st][2 + half]);
-                    split_tf32(x.z, qf[st + 1][half], ql[st + 1][half]);
-                    split_tf32(x.w, qf[st + 1][2 + half], ql[st + 1][2 + half]);
+                    qf[st][half] = __float_as_uint(x.x);
+                    qf[st][2 + half] = __float_as_uint(x.y);
+                    qf[st + 1][half] = __float_as_uint(x.z);
+                    qf[st + 1][2 + half] = __float_as_uint(x.w);
                 }
             }
         }
@@ -423,140 +551,88 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
         }
     }
 
-    // Joins cnt pieces, the i-th in workspace slot slot(i): all heads' statistics, then o. The result goes to
-    // the group's output, or back into the workspace at `to`.
-    auto join = [&](int cnt, auto slot, int64_t head, float *to) {
-        auto piece = [&](int i) { return parts + (int64_t)slot(i) * piece_floats(a.G, D); };
-        const int jh = tid & 15, ji = tid >> 4;
-        float2 ml[kSetMax / 8];
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int e = 0; e < kSetMax / 8; ++e) {
-            const int i = ji + 8 * e;
-            ml[e] = i < cnt && jh < a.G ? __ldcg(reinterpret_cast<const float2 *>(piece(i)) + jh) : make_float2(-INFINITY, 0.f);
-            M = max_nan(M, ml[e].x);
-        }
-        sm.mx[ji][jh] = M;
-        math_sync();
-        M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) M = max_nan(M, sm.mx[w][jh]);
-#pragma unroll
-        for (int e = 0; e < kSetMax / 8; ++e) {
-            const float f = ml[e].x == -INFINITY ? 0.f : ex2(ml[e].x - M);
-            sm.weight[ji + 8 * e][jh] = f;
-            L += f == 0.f ? 0.f : ml[e].y * f;
-        }
-        sm.sum[ji][jh] = L;
-        math_sync();
-        auto total = [&](int h) {
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) s += sm.sum[w][h];
-            return s;
-        };
-        constexpr int ITEMS = kRows * D / 4 / kMath;
-        float4 acc[ITEMS];
-#pragma unroll
-        for (int e = 0; e < ITEMS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int items = a.G * (D / 4);
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-            const float4 *src = reinterpret_cast<const float4 *>(piece(i) + piece_ml(a.G));
-#pragma unroll
-            for (int e = 0; e < ITEMS; ++e) {
-                const int at = tid + e * kMath;
-                if (at < items) {
-                    const float4 v = __ldcg(src + at);
-                    const float f = sm.weight[i][at / (D / 4)];
-                    // a piece without weight may hold anything
-                    acc[e].x = f == 0.f ? acc[e].x : fmaf(v.x, f, acc[e].x);
-                    acc[e].y = f == 0.f ? acc[e].y : fmaf(v.y, f, acc[e].y);
-                    acc[e].z = f == 0.f ? acc[e].z : fmaf(v.z, f, acc[e].z);
-                    acc[e].w = f == 0.f ? acc[e].w : fmaf(v.w, f, acc[e].w);
-                }
-            }
-        }
-        if (to) math_sync();               // everyone has read piece 0, which the result replaces
-#pragma unroll
-        for (int e = 0; e < ITEMS; ++e) {
-            const int at = tid + e * kMath, h = at / (D / 4);
-            if (at >= items) continue;
-            if (to) {
-                reinterpret_cast<float4 *>(to + piece_ml(a.G))[at] = acc[e];
-            } else {
-                const float l = total(h), v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
-                float y[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = l == 0.f ? 0.f : v[c] / l;
-                store_vec<4>(static_cast<T *>(a.out) + head * D + (int64_t)at * 4, y);
-            }
-        }
-        if (ji == 0 && jh < a.G) {
-            const float l = total(jh);
-            if (to) reinterpret_cast<float2 *>(to)[jh] = make_float2(M, l);
-            else if (a.lse) a.lse[head + jh] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
-        }
-    };
     // Announces this CTA's piece (or set of pieces) at a counter; true in the CTA that is the last of `of`.
+    // (The barrier puts every thread's stores before thread 0's fence, which publishes them; the pieces are
+    // read past L1.)
     auto arrive = [&](int32_t *counter, int of) {
-        __threadfence();
         math_sync();
         if (tid == 0) {
-            sm.last = atomicAdd(counter, 1) == of - 1;
-            if (sm.last) *counter = 0;
+            __threadfence();
+            const bool last = atomicAdd(counter, 1) == of - 1;
+            if (last) {
+                __threadfence();
+                *counter = 0;
+            }
+            sm.last = last;
         }
         math_sync();
-        const bool last = sm.last;
-        if (last) __threadfence();
-        return last;
+        return sm.last != 0;
     };
 
+    int seg = -1;
     for (int it = 0; it < n; ++it) {
         const int st = it % kStages;
         const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
         const Tile d = sm.tile[st];
-        if ((d.flags & kFirst) && ok) load_q(d.r, d.kvh);
+        if (d.flags & kFirst) {
+            ++seg;
+            load_q(seg % S::QS);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[seg % S::QS]));
+        }
         const uint32_t kt = smem_u32(sm.ring[st]), vt = kt + kTileBytes;
         const uint8_t *ktp = sm.ring[st], *vtp = ktp + kTileBytes;
 
         // ---- S = Q K^T of this warp's tokens
         float x[NT][4];
+        if constexpr (kBf16) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int blk = nt * 8 * ROWB;
-            if constexpr (kBf16) {
+            for (int nt = 0; nt < NT; ++nt) {
                 float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int kp = 0; kp < D / 32; ++kp) {
                     uint32_t b[4];
-                    ldsm4(kt + ko[kp & 1] + blk + (kp >> 1) * 1024, b);
+                    ldsm4(kt + ko[kp & 1] + nt * 8 * ROWB + (kp >> 1) * 1024, b);
                     mma_bf16(s0, qf[2 * kp], b[0], b[1]);
                     mma_bf16(s1, qf[2 * kp + 1], b[2], b[3]);
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) x[nt][u] = (s0[u] + s1[u]) * s2;
-            } else {
-                // three tf32 products (the low parts' product, 2^-22 of the whole, is left out)
-                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f}, cr[4] = {0.f, 0.f, 0.f, 0.f};
+            }
+        } else {
+            // three tf32 products (the low parts' product, 2^-22 of the whole, is left out)
+            float s0[NT][4], s1[NT][4], cr[NT][4];
 #pragma unroll
-                for (int kp = 0; kp < D / 16; ++kp) {
-                    const float4 kx = *reinterpret_cast<const float4 *>(ktp + ko[kp & 1] + blk + (kp >> 1) * 1024);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) s0[nt][u] = s1[nt][u] = cr[nt][u] = 0.f;
+#pragma unroll
+            for (int kp = 0; kp < D / 16; ++kp) {
+                uint32_t qh[2][4], ql[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) split_tf32(__uint_as_float(qf[2 * kp + e][u]), qh[e][u], ql[e][u]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 kx = *reinterpret_cast<const float4 *>(ktp + ko[kp & 1] + nt * 8 * ROWB + (kp >> 1) * 1024);
                     uint32_t h[4], w[4];
                     split_tf32(kx.x, h[0], w[0]);
                     split_tf32(kx.y, h[1], w[1]);
                     split_tf32(kx.z, h[2], w[2]);
                     split_tf32(kx.w, h[3], w[3]);
-                    mma_tf32(s0, qf[2 * kp], h[0], h[1]);
-                    mma_tf32(s1, qf[2 * kp + 1], h[2], h[3]);
-                    mma_tf32(cr, qf[2 * kp], w[0], w[1]);
-                    mma_tf32(cr, ql[2 * kp], h[0], h[1]);
-                    mma_tf32(cr, qf[2 * kp + 1], w[2], w[3]);
-                    mma_tf32(cr, ql[2 * kp + 1], h[2], h[3]);
+                    mma_tf32(s0[nt], qh[0], h[0], h[1]);
+                    mma_tf32(s1[nt], qh[1], h[2], h[3]);
+                    mma_tf32(cr[nt], qh[0], w[0], w[1]);
+                    mma_tf32(cr[nt], ql[0], h[0], h[1]);
+                    mma_tf32(cr[nt], qh[1], w[2], w[3]);
+                    mma_tf32(cr[nt], ql[1], h[2], h[3]);
                 }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) x[nt][u] = with_correction(s0[u] + s1[u], cr[u]) * s2;
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[nt][u] = with_correction(s0[nt][u] + s1[nt][u], cr[nt][u]) * s2;
         }
         if (d.flags & kEdge) {
             // tokens outside the row's range or on no page: no score, and a zero value row
@@ -748,23 +824,29 @@ paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, con
 
         // ---- the last piece to arrive joins them all; with many pieces the last of a set of about sqrt(pieces)
         // joins the set into its first piece's place, and the last set to arrive joins the sets
-        const int c_first = (int)(((d.g0 + 1) * P - 1) / W), c_last = (int)(((d.g0 + d.len) * P - 1) / W);
+        const int c_first = (int)quot((d.g0 + 1) * P - 1, W), c_last = (int)quot((d.g0 + d.len) * P - 1, W);
         const int pieces = c_last - c_first + 1, mine_i = (int)blockIdx.x - c_first;
-        const int slot0 = 2 * c_first + (W * c_first / P < d.g0 ? 1 : 0);
-        auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (c_first + i); };
+        const int slot0 = 2 * c_first + (quot(W * c_first, P) < d.g0 ? 1 : 0);
         int set = pieces;
         if (pieces > kDirect) {
             set = kDirect / 2;
             while (set * set < pieces) ++set;
         }
         const int i0 = mine_i / set * set, in_set = min(set, pieces - i0), sets = (pieces + set - 1) / set;
-        if (!arrive(arrived + slot(i0), in_set)) continue;
-        if (sets == 1) {
-            join(pieces, slot, head, nullptr);
-        } else {
-            join(in_set, [&](int i) { return slot(i0 + i); }, head, parts + (int64_t)slot(i0) * piece_floats(a.G, D));
-            if (arrive(arrived + 2 * kMaxWorkers + slot0, sets))
-                join(sets, [&](int i) { return slot(i * set); }, head, nullptr);
+        const int set0 = i0 == 0 ? slot0 : 2 * (c_first + i0);
+        int32_t *counter = arrived + set0;
+        int cnt = in_set, s0 = set0, s1 = 2 * (c_first + i0 + 1), step = 2;
+        bool back = sets > 1;
+#pragma unroll 1
+        while (arrive(counter, cnt)) {
+            join<T, D>(a, parts, sm, cnt, s0, s1, step, head, back);
+            if (!back) break;
+            counter = arrived + 2 * kMaxWorkers + slot0;       // now the sets
+            cnt = sets;
+            s0 = slot0;
+            s1 = 2 * (c_first + set);
+            step = 2 * set;
+            back = false;
         }
         math_sync();                       // shared memory of the join before the next tile's
     }
