@@ -236,8 +236,9 @@ zha_status zha_paged_decode(const zha_paged_config *cfg, int32_t n_rows, const v
     if (s != ZHA_OK) return s;
     if (n_rows < 0 || (!seq_ids && n_rows > cfg->batch)) return ZHA_ERR_INVALID_ARG;
     if (n_rows == 0) return ZHA_OK;
-    // rows * heads and every query offset in int32, tile counts in int64
+    // counts of query heads and of tiles (of 32 tokens at least) in int32
     if ((int64_t)n_rows * cfg->n_q_heads > (1 << 24)) return ZHA_ERR_UNSUPPORTED;
+    if ((int64_t)n_rows * cfg->n_kv_heads > (int64_t(1) << 35) / cfg->page_size / cfg->max_pages) return ZHA_ERR_UNSUPPORTED;
     if (!q || !kpool || !vpool || !table || !lens || !out || !workspace) return ZHA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) || !aligned16(workspace))
         return ZHA_ERR_INVALID_ARG;

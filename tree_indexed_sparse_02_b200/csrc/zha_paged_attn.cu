@@ -44,7 +44,7 @@ constexpr int kMaxWorkers = 148 * 2;
 constexpr int kMinTiles = 4;             // tiles of a CTA's part at least
 constexpr int kBox = 16;                 // rows of a page copied at a time, at most
 constexpr int kDirect = 16;              // pieces of a group joined at once; more in two levels
-constexpr int kSetMax = 24;              // ceil(sqrt(kMaxWorkers)) rounded up to a multiple of 8
+constexpr int kSnap = 2;                 // a CTA's part begins at a group's border if one is this near (in tiles)
 constexpr long long kWaitCycles = 4000000000ll;   // ~2 s: a wait that long is an error
 
 // The tokens [lo, hi) that row r attends and the sequence they belong to
@@ -138,11 +138,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// a / b, in 32 bits where both fit (a 64-bit division takes hundreds of cycles)
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 // A piece of a group in the workspace: (m, l) of its G heads, padded to whole
 // float4s, then o as [G][D].
 __host__ __device__ __forceinline__ int piece_ml(int G) { return (2 * G + 3) & ~3; }
@@ -151,14 +146,14 @@ __host__ __device__ __forceinline__ int piece_floats(int G, int d) { return piec
 // One tile of a group, as the copying warp describes it to the others.
 struct Tile {
     int r, kvh;
-    int len;          // tiles of the group
     int flags;
-    int64_t g0;       // the group's first tile in the list of all tiles
     int base, lo, hi; // first token, and the tokens the row attends
+    int c_first, pieces;      // a split group's last tile here: the first CTA that has a piece of it, and how many do
     uint32_t bad[4];  // tokens whose page number is no page
 };
-// of this CTA's piece of the group: its first and last tile; the piece is the group; some token is not attended
-enum { kFirst = 1, kLast = 2, kWhole = 4, kEdge = 8 };
+// first and last tile of this CTA's piece of the group; the piece begins and ends with the group; some token is
+// not attended
+enum { kFirst = 1, kLast = 2, kHead = 4, kTail = 8, kEdge = 16 };
 
 template <typename T, int D>
 struct Shared {
@@ -170,93 +165,78 @@ struct Shared {
     // P in two parts: weights keep 16 (bf16) or 22 (tf32) bits; one bf16 part alone would cost half an
     // ulp of the output
     typedef typename std::conditional<sizeof(T) == 2, __nv_bfloat16, float>::type PT;
-    union {
-        alignas(16) PT p[2][kRows][PS];
-        float weight[kSetMax][kRows];
-    };
+    alignas(16) PT p[2][kRows][PS];
     static constexpr int QROW = D * (int)sizeof(T) + 16;           // padded: no bank twice
     static constexpr int QS = sizeof(T) == 2 ? 2 : 1;              // places for the queries of a piece
     alignas(16) uint8_t q[QS][kRows][QROW];
     Tile tile[kStages];
-    float mx[2 * kWarps][kRows], sum[2 * kWarps][kRows];
-    int64_t scan[kThreads / 32];
-    int64_t start_before;
+    float mx[kWarps][kRows], sum[kWarps][kRows];
+    int scan[kThreads / 32];
+    // of the rows that this part's two ends fall into: the row, tiles before it, its own tiles (of each head)
+    int edge_row[2], edge_before[2], edge_tiles[2];
     uint64_t full[kStages], empty[kStages], q_empty[QS];
-    int start_row, last, abort;
+    int last, abort;
 };
 
-// Joins cnt pieces in slots s0, s1, s1 + step, ... of the workspace: all heads' statistics, then o. The
-// result goes to the group's output, or back into slot s0.
+// Joins cnt pieces in slots s0, s1, s1 + step, ... of the workspace, eight at a time; the result goes to the
+// group's output, or back into slot s0. Each thread does its float4s of the heads' o with a running maximum of
+// its own, so that nothing waits but for the loads. (Small code on purpose: it runs once or twice in a CTA's
+// life, from a cold instruction cache.)
 template <typename T, int D>
-__device__ __forceinline__ void join(const PagedAttnArgs &a, float *parts, Shared<T, D> &sm, int cnt, int s0, int s1, int step,
-                              int64_t head, bool back) {
-    const int tid = threadIdx.x;
-    auto piece = [&](int i) { return parts + (int64_t)(i == 0 ? s0 : s1 + (i - 1) * step) * piece_floats(a.G, D); };
-    float *to = back ? piece(0) : nullptr;
-    constexpr int FLY = 8;             // loads in flight
-    const int items = a.G * (D / 4);
-    const int jh = tid & 15, ji = tid >> 4;
-    float2 ml[kSetMax / 8];
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int e = 0; e < kSetMax / 8; ++e) {
-        const int i = ji + 8 * e;
-        ml[e] = i < cnt && jh < a.G ? __ldcg(reinterpret_cast<const float2 *>(piece(i)) + jh) : make_float2(-INFINITY, 0.f);
-    }
-#pragma unroll
-    for (int e = 0; e < kSetMax / 8; ++e) M = max_nan(M, ml[e].x);
-    sm.mx[ji][jh] = M;
-    math_sync();
-    M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) M = max_nan(M, sm.mx[w][jh]);
-#pragma unroll
-    for (int e = 0; e < kSetMax / 8; ++e) {
-        const float f = ml[e].x == -INFINITY ? 0.f : ex2(ml[e].x - M);
-        sm.weight[ji + 8 * e][jh] = f;
-        L += f == 0.f ? 0.f : ml[e].y * f;
-    }
-    sm.sum[ji][jh] = L;
-    math_sync();
-    auto total = [&](int h) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) s += sm.sum[w][h];
-        return s;
-    };
-    // small code on purpose: it runs once or twice in a CTA's life, from a cold instruction cache
+__device__ __forceinline__ void join(const PagedAttnArgs &a, float *parts, int cnt, int s0, int s1, int step, int64_t head,
+                                     bool back) {
+    constexpr int FLY = 8, Q = D / 4;          // float4s of a head
+    const int items = a.G * Q, pf = piece_floats(a.G, D);
+    float *first = parts + (int64_t)s0 * pf;
 #pragma unroll 1
-    for (int at = tid; at < items; at += kMath) {
-        const int h = at / (D / 4);
+    for (int base = threadIdx.x & ~31; base < items; base += kMath) {
+        // a head's float4s are lanes of one warp
+        const bool mine = base + (threadIdx.x & 31) < items;
+        const int at = mine ? base + (threadIdx.x & 31) : items - 1, h = at / Q;
+        float M = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (int i0 = 0; i0 < cnt; i0 += FLY) {
             float4 v[FLY];
-#pragma unroll
-            for (int u = 0; u < FLY; ++u)
-                v[u] = __ldcg(reinterpret_cast<const float4 *>(piece(min(i0 + u, cnt - 1)) + piece_ml(a.G)) + at);
+            float2 ml[FLY];
 #pragma unroll
             for (int u = 0; u < FLY; ++u) {
-                const float f = i0 + u < cnt ? sm.weight[i0 + u][h] : 0.f;
-                if (f == 0.f) continue;    // a piece without weight may hold anything
+                const int i = i0 + u;
+                const float *piece = i == 0 || i >= cnt ? first : parts + (int64_t)(s1 + (i - 1) * step) * pf;
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(piece) + h);
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(piece + piece_ml(a.G)) + at);
+                if (i >= cnt) ml[u] = make_float2(-INFINITY, 0.f);
+            }
+            float mx = M;
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) mx = max_nan(mx, ml[u].x);
+            const float ref = mx == -INFINITY ? 0.f : mx, c = ex2(M - ref);
+            M = mx;
+            L *= c;
+            acc.x *= c;
+            acc.y *= c;
+            acc.z *= c;
+            acc.w *= c;
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) {
+                if (ml[u].x == -INFINITY) continue;        // a piece without weight
+                const float f = ex2(ml[u].x - ref);
+                L = fmaf(ml[u].y, f, L);
                 acc.x = fmaf(v[u].x, f, acc.x);
                 acc.y = fmaf(v[u].y, f, acc.y);
                 acc.z = fmaf(v[u].z, f, acc.z);
                 acc.w = fmaf(v[u].w, f, acc.w);
             }
         }
-        if (to) {                          // over piece 0, whose quarter of a row only this thread reads
-            reinterpret_cast<float4 *>(to + piece_ml(a.G))[at] = acc;
-        } else {
-            const float inv = 1.f / total(h), y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-            store_vec<4>(static_cast<T *>(a.out) + head * D + (int64_t)at * 4, total(h) == 0.f ? zero : y);
+        if (back) {
+            __syncwarp();                          // piece s0 has been read
+            if (mine) reinterpret_cast<float4 *>(first + piece_ml(a.G))[at] = acc;
+            if (mine && at % Q == 0) reinterpret_cast<float2 *>(first)[h] = make_float2(M, L);
+        } else if (mine) {
+            const float inv = L == 0.f ? 0.f : 1.f / L, y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+            store_vec<4>(static_cast<T *>(a.out) + head * D + (int64_t)at * 4, y);
+            if (a.lse && at % Q == 0) a.lse[head + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         }
-    }
-    if (ji == 0 && jh < a.G) {
-        const float l = total(jh);
-        if (to) reinterpret_cast<float2 *>(to)[jh] = make_float2(M, l);
-        else if (a.lse) a.lse[head + jh] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
     }
 }
 
@@ -298,64 +278,96 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     const bool few = a.rows <= 32;
     const int per = few ? 1 : (a.rows + kThreads - 1) / kThreads;
     const int ra = min((few ? lane : tid) * per, a.rows), rb = min(ra + per, a.rows);
-    int64_t mine = 0;
+    int mine = 0;
     for (int r = ra; r < rb; ++r) mine += tiles_of(row_span(a, r));
-    int64_t incl = mine;
+    int before = mine;                   // first inclusive, of this warp's lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
     }
-    int64_t before = incl - mine, all = 0;
-    if (few) {
-        all = __shfl_sync(0xffffffffu, incl, 31);
-    } else {
-        if (lane == 31) sm.scan[warp] = incl;
+    int W = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    if (!few) {
+        if (lane == 0) sm.scan[warp] = W;
         __syncthreads();
-#pragma unroll
+        W = 0;
+#pragma unroll 1
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += sm.scan[w];
-            all += sm.scan[w];
+            W += sm.scan[w];
         }
     }
-    const int64_t W = all * a.Hkv;
-    const int64_t want = (W + kMinTiles - 1) / kMinTiles;
-    const int P = want < gridDim.x ? (int)want : (int)gridDim.x;    // CTAs that get a part
-    const int64_t w0 = (int)blockIdx.x < P ? quot(W * blockIdx.x, P) : 0;
-    const int64_t w1 = (int)blockIdx.x < P ? quot(W * (blockIdx.x + 1), P) : 0;
-    const int n = (int)(w1 - w0);
-    if (n > 0 && (!few || warp == kWarps) && w0 >= before * a.Hkv && w0 < (before + mine) * a.Hkv) {
-        int64_t at = before;
-        for (int r = ra; r < rb; ++r) {
-            const int t = tiles_of(row_span(a, r));
-            if (w0 < (at + t) * a.Hkv) {
-                sm.start_row = r;
-                sm.start_before = at;
-                break;
+    W *= a.Hkv;
+    // Parts of `share` tiles, their ends moved to a group's border where one is within kSnap tiles: a piece of a
+    // few tiles costs more to join than to compute.
+    const int share = max(kMinTiles, (W + (int)gridDim.x - 1) / (int)gridDim.x);
+    int w0 = 0, w1 = 0, start_row = 0, start_before = 0;
+    const int first_tile = min((int64_t)blockIdx.x * share, (int64_t)W);
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {        // (a loop, not two copies: the code is cold)
+        int edge = e ? min(first_tile + share, W) : first_tile;
+        const bool own = edge >= before * a.Hkv && edge < (before + mine) * a.Hkv;
+        int row = ra, t = mine, at = before;
+        if (few) {
+            const int src = (__ffs(__ballot_sync(0xffffffffu, own)) - 1) & 31;
+            row = __shfl_sync(0xffffffffu, ra, src);
+            t = __shfl_sync(0xffffffffu, mine, src);
+            at = __shfl_sync(0xffffffffu, before, src);
+        } else {
+            if (own) {
+                for (row = ra; row < rb; ++row) {
+                    t = tiles_of(row_span(a, row));
+                    if (edge < (at + t) * a.Hkv) break;
+                    at += t;
+                }
+                sm.edge_row[e] = row;
+                sm.edge_tiles[e] = t;
+                sm.edge_before[e] = at;
             }
-            at += t;
+            __syncthreads();
+            row = sm.edge_row[e];
+            t = sm.edge_tiles[e];
+            at = sm.edge_before[e];
         }
+        if (e == 0) {
+            start_row = row;
+            start_before = at;
+        }
+        if (edge > 0 && edge < W) {
+            const int i = (edge - at * a.Hkv) % t;
+            if (t - i <= kSnap) edge += t - i;
+            else if (i <= kSnap) edge -= i;
+        }
+        if (e == 0) w0 = edge;
+        else w1 = edge;
     }
-    if (few) __syncwarp();
-    else __syncthreads();
+    const int n = w1 - w0;
 
     if (warp == kWarps) {
         // ================= the copying warp
         if (n == 0) return;
         // where a walk over the list stands: tile i of the group (r, kvh), whose len tiles begin at g0
         struct Walk {
-            int r, kvh, i, len;
-            int64_t g0;
+            int r, kvh, i, len, g0;
             RowSpan span;
         };
         Walk next;
-        next.r = sm.start_row;
+        next.r = start_row;
         next.span = row_span(a, next.r);
         next.len = tiles_of(next.span);
-        next.g0 = sm.start_before * a.Hkv;
-        next.kvh = (int)quot(w0 - next.g0, next.len);
-        next.g0 += (int64_t)next.kvh * next.len;
-        next.i = (int)(w0 - next.g0);
+        next.g0 = start_before * a.Hkv;
+        next.kvh = (w0 - next.g0) / next.len;
+        next.g0 += next.kvh * next.len;
+        next.i = w0 - next.g0;
+        auto next_row = [&]() {
+            next.kvh = 0;
+            do {
+                next.span = row_span(a, ++next.r);
+                next.len = tiles_of(next.span);
+            } while (next.len == 0);
+        };
+        if (next.kvh == a.Hkv) next_row();         // the start moved up to the end of its row
         // A lane looks up one box's page of one of the next `batch` tiles of a group (TMA), or the pages of
         // the tokens lane, lane + 32, ... of the next tile (small pages), a batch ahead of the copies.
         constexpr int NP = kTma ? 1 : TT / 32;
@@ -390,13 +402,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     if (next.i == next.len) {
                         next.i = 0;
                         next.g0 += next.len;
-                        if (++next.kvh == a.Hkv) {
-                            next.kvh = 0;
-                            do {
-                                next.span = row_span(a, ++next.r);
-                                next.len = tiles_of(next.span);
-                            } while (next.len == 0);
-                        }
+                        if (++next.kvh == a.Hkv) next_row();
                     }
                     look();
                 }
@@ -405,14 +411,18 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             Tile d;
             d.r = c.r;
             d.kvh = c.kvh;
-            d.len = c.len;
-            d.g0 = c.g0;
             d.base = (c.span.lo & -box) + ci * TT;
             d.lo = c.span.lo;
             d.hi = c.span.hi;
             d.flags = ((k == 0 || ci == 0) ? kFirst : 0) | ((k == n - 1 || ci == c.len - 1) ? kLast : 0) |
-                      ((c.g0 >= w0 && c.g0 + c.len <= w1) ? kWhole : 0) |
+                      (c.g0 >= w0 ? kHead : 0) | (c.g0 + c.len <= w1 ? kTail : 0) |
                       ((d.base < d.lo || d.base + TT > d.hi) ? kEdge : 0);
+            if ((d.flags & kLast) && (d.flags & (kHead | kTail)) != (kHead | kTail)) {
+                // the parts that begin inside the group, not near its borders
+                const int lo = (c.g0 + kSnap) / share + 1, hi = (c.g0 + c.len - kSnap - 1) / share;
+                d.c_first = lo - 1;
+                d.pieces = hi - lo + 2;
+            }
             d.bad[0] = d.bad[1] = d.bad[2] = d.bad[3] = 0;
             int64_t row[NP];               // first row of the copy in its pool, -1: none
 #pragma unroll
@@ -788,8 +798,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         math_sync();
         const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
         float *part = nullptr;
-        if (!(d.flags & kWhole))           // slot 2c: the piece that begins with CTA c's part; 2c + 1: its other one
-            part = parts + (2 * (int64_t)blockIdx.x + (d.g0 > w0 ? 1 : 0)) * piece_floats(a.G, D);
+        if ((d.flags & (kHead | kTail)) != (kHead | kTail))        // slot 2c + 1: a group's first piece, 2c: another
+            part = parts + (2 * (int64_t)blockIdx.x + (d.flags & kHead ? 1 : 0)) * piece_floats(a.G, D);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float L = 0.f;
@@ -824,31 +834,28 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
 
         // ---- the last piece to arrive joins them all; with many pieces the last of a set of about sqrt(pieces)
         // joins the set into its first piece's place, and the last set to arrive joins the sets
-        const int c_first = (int)quot((d.g0 + 1) * P - 1, W), c_last = (int)quot((d.g0 + d.len) * P - 1, W);
-        const int pieces = c_last - c_first + 1, mine_i = (int)blockIdx.x - c_first;
-        const int slot0 = 2 * c_first + (quot(W * c_first, P) < d.g0 ? 1 : 0);
+        const int pieces = d.pieces, slot0 = 2 * d.c_first + 1, mine_i = (int)blockIdx.x - d.c_first;
         int set = pieces;
         if (pieces > kDirect) {
             set = kDirect / 2;
             while (set * set < pieces) ++set;
         }
         const int i0 = mine_i / set * set, in_set = min(set, pieces - i0), sets = (pieces + set - 1) / set;
-        const int set0 = i0 == 0 ? slot0 : 2 * (c_first + i0);
+        const int set0 = i0 == 0 ? slot0 : 2 * (d.c_first + i0);
         int32_t *counter = arrived + set0;
-        int cnt = in_set, s0 = set0, s1 = 2 * (c_first + i0 + 1), step = 2;
+        int cnt = in_set, s0 = set0, s1 = 2 * (d.c_first + i0 + 1), step = 2;
         bool back = sets > 1;
 #pragma unroll 1
         while (arrive(counter, cnt)) {
-            join<T, D>(a, parts, sm, cnt, s0, s1, step, head, back);
+            join<T, D>(a, parts, cnt, s0, s1, step, head, back);
             if (!back) break;
             counter = arrived + 2 * kMaxWorkers + slot0;       // now the sets
             cnt = sets;
             s0 = slot0;
-            s1 = 2 * (c_first + set);
+            s1 = 2 * (d.c_first + set);
             step = 2 * set;
             back = false;
         }
-        math_sync();                       // shared memory of the join before the next tile's
     }
     // ---- rows that attend nothing
     for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
