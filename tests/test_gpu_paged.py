@@ -377,6 +377,34 @@ def test_decode_special_values(zha, dt):
     assert torch.equal(out[4], good[0][4])
 
 
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_keeps_other_results_when_some_are_not_finite(zha, dt, d):
+    """An infinite value makes its own coordinate infinite, a head whose query is NaN only itself NaN, and garbage of
+    every kind behind the sequence's end does nothing: all other results keep their bits."""
+    lens = [150, 151, 40]
+    for poison in (0.0, float("nan"), float("inf"), -3e38):
+        c = Case(zha, lens, 8, 1, d, 16, dt, seed=16, poison=poison)
+        q = c.queries(3)
+        out, lse = c.run(q)
+        c.check(q, out, lse, [(b, b, n) for b, n in enumerate(lens)])
+        if poison == 0.0:
+            good = out, lse
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    c.v[c.table[0, 2], 0, 3, 5] = float("inf")
+    c.v[c.table[0, 2], 0, 4, 6] = -float("inf")
+    q[1, 3] = float("nan")
+    out, lse = c.run(q)
+    assert torch.all(out[0, :, 5] == float("inf")) and torch.all(out[0, :, 6] == -float("inf"))
+    assert torch.all(torch.isnan(out[1, 3])) and torch.isnan(lse[1, 3])
+    rest = torch.ones_like(out, dtype=torch.bool)
+    rest[0, :, 5:7] = rest[1, 3] = False
+    assert torch.equal(out[rest], good[0][rest])
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[1, 3] = False
+    assert torch.equal(lse[keep], good[1][keep])
+
+
 def test_decode_scale_and_peaked_scores(zha):
     lens = [1500, 90]
     for scale, amp in ((0.5, 4.0), (1.0, 0.01), (1e-3, 1.0)):

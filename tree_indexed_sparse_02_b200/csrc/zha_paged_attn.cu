@@ -644,24 +644,17 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
 #pragma unroll
                 for (int u = 0; u < 4; ++u) x[nt][u] = with_correction(s0[nt][u] + s1[nt][u], cr[nt][u]) * s2;
         }
+        // tokens outside the row's range or on no page
+        auto hidden = [&](int t) {
+            const int pos = d.base + t;
+            return pos < d.lo || pos >= d.hi || ((sm.tile[st].bad[t >> 5] >> (t & 31)) & 1u);
+        };
         if (d.flags & kEdge) {
-            // tokens outside the row's range or on no page: no score, and a zero value row
-            auto hidden = [&](int t) {
-                const int pos = d.base + t;
-                return pos < d.lo || pos >= d.hi || ((sm.tile[st].bad[t >> 5] >> (t & 31)) & 1u);
-            };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     if (hidden(tok0 + nt * 8 + tok_of(u & 1))) x[nt][u] = -INFINITY;
-            for (int i = tid; i < TT * CH; i += kMath) {
-                const int t = i / CH, ch = i % CH;         // (the order of a row's chunks does not matter)
-                if (hidden(t))
-                    *reinterpret_cast<uint4 *>(sm.ring[st] + kTileBytes + (t >> 3) * 8 * ROWB + (ch >> 3) * 1024 +
-                                               (t & 7) * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();      // before a later copy lands there
         }
         // ---- row maxima over the tile
 #pragma unroll
@@ -708,8 +701,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         }
         math_sync();
         // ---- the tile's P V in accumulators of its own (the MMA truncates its sums: kept short), then into O.
-        // A non-finite value times a low part can be NaN where the product is infinite: such a tile is
-        // done again with the high parts alone.
         float pv[NJ][4];
         auto weigh = [&](bool low) {
 #pragma unroll
@@ -778,7 +769,38 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int u = 0; u < 4; ++u) odd = fmaf(pv[j][u], 0.f, odd);
-        if (__any_sync(0xffffffffu, odd != 0.f)) weigh(false);
+        if (__any_sync(0xffffffffu, odd != 0.f)) {
+            // Hidden tokens have weight 0, but whatever their value rows hold (other sequences' rows, NaN) was
+            // multiplied by it: clear them and do the tile again. An attended infinite value times a low part
+            // can be NaN where the product is infinite: what is not finite then is taken from the high parts.
+            if (d.flags & kEdge)
+                for (int i = lane; i < TT * CH / 4; i += 32) {     // this warp's coordinates, which no other reads
+                    const int t = i / (CH / 4), ch = warp * (CH / 4) + i % (CH / 4);
+                    if (hidden(t))
+                        *reinterpret_cast<uint4 *>(sm.ring[st] + kTileBytes + (t >> 3) * 8 * ROWB + (ch >> 3) * 1024 +
+                                                   (t & 7) * 128 + (((ch & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+            __syncwarp();
+            weigh(true);
+            odd = 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) odd = fmaf(pv[j][u], 0.f, odd);
+            if (__any_sync(0xffffffffu, odd != 0.f)) {
+                float both[NJ][4];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) both[j][u] = pv[j][u];
+                weigh(false);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) pv[j][u] = fabsf(both[j][u]) <= 3.0e38f ? both[j][u] : pv[j][u];
+            }
+            fence_proxy_async_smem();      // before a later copy lands there
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
 #pragma unroll
