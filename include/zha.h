@@ -420,7 +420,7 @@ ZHA_API zha_status zha_paged_check_config(const zha_paged_config *cfg);
  * position 0, slot -1 and sequence -1. */
 typedef struct zha_token_map {
     int32_t *positions, *slots, *seq_ids, *cu_new;
-    int32_t max_tokens;  /* rows of the token buffer */
+    int32_t max_tokens;  /* rows of the token buffer, at most 2^30 */
     int32_t reserved;
 } zha_token_map;
 
@@ -540,7 +540,12 @@ ZHA_API size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_
  * ZHA_ERR_INVALID_ARG and its tokens are skipped. Cache rows outside the
  * attended range are not read into any result, whatever they hold. Softmax
  * statistics and sums are fp32. The result does not depend on timing (a split
- * row's parts are joined in a fixed order).
+ * row's parts are joined in a fixed order). A row whose every score is -inf
+ * gets zeros and -inf as well. Every wait inside is bounded (about two
+ * seconds): ZHA_ERR_TIMEOUT, the results are then invalid and the workspace is
+ * to be zeroed again. n_rows * n_q_heads <= 2^24 and
+ * n_rows * n_kv_heads * max_pages * page_size <= 2^35, otherwise
+ * ZHA_ERR_UNSUPPORTED.
  */
 ZHA_API zha_status zha_paged_decode(const zha_paged_config *cfg, int32_t n_rows, const void *q,
                                     const void *kpool, const void *vpool, const int32_t *table,

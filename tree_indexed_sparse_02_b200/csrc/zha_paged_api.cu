@@ -82,6 +82,7 @@ zha_status zha_paged_plan(const zha_paged_config *cfg, int32_t *table, const int
         return ZHA_ERR_INVALID_ARG;
     if (!map->positions || !map->slots || !map->seq_ids || !map->cu_new || map->max_tokens < 1 || map->reserved)
         return ZHA_ERR_INVALID_ARG;
+    if (map->max_tokens > (1 << 30)) return ZHA_ERR_UNSUPPORTED;
     zha::PlanArgs a{};
     a.B = cfg->batch;
     a.lps = log2i(cfg->page_size);

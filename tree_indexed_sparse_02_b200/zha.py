@@ -8,6 +8,7 @@ is missing the import fails loudly (there is no fallback path).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -25,6 +26,7 @@ ZHA_SUMMARY_NATIVE, ZHA_SUMMARY_MXFP8 = 0, 1
 ZHA_ROPE_HALF, ZHA_ROPE_INTERLEAVED = 0, 1
 ZHA_ROPE_PLAIN, ZHA_ROPE_LINEAR, ZHA_ROPE_NTK, ZHA_ROPE_YARN = 0, 1, 2, 3
 ZHA_MAX_LEVELS = 8
+_DTYPES = {torch.bfloat16: ZHA_BF16, torch.float32: ZHA_F32}
 STATUS_NAMES = {0: "ZHA_OK", 1: "ZHA_ERR_INVALID_ARG", 2: "ZHA_ERR_UNSUPPORTED",
                 3: "ZHA_ERR_CAPACITY", 4: "ZHA_ERR_CUDA", 5: "ZHA_ERR_TIMEOUT"}
 
@@ -67,9 +69,25 @@ class PagedConfig(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("window", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
 
-    @property
+    # What the calls need of a configuration every time, made once (a configuration is not changed after its first
+    # call: make another).
+    @functools.cached_property
     def torch_dtype(self):
         return torch.bfloat16 if self.dtype == ZHA_BF16 else torch.float32
+
+    @functools.cached_property
+    def ref(self):
+        return ctypes.byref(self)
+
+    @functools.cached_property
+    def pool_elements(self):
+        return self.n_pages * self.n_kv_heads * self.page_size * self.head_dim
+
+    def decode_workspace(self, rows):
+        known = self.__dict__.setdefault("_workspace", {})
+        if rows not in known:
+            known[rows] = int(_lib.zha_paged_workspace_bytes(self.ref, rows)) if rows else 0
+        return known[rows]
 
 
 class TokenMap(ctypes.Structure):
@@ -289,46 +307,52 @@ def paged_workspace(cfg: PagedConfig, rows: int, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _refuse(where: str, what: str):
-    raise ValueError(f"{where}: {what}")
+# The checks below are on the path of every call, whose kernels can take less time than their launch: they read
+# few tensor attributes, and the messages are made only where one fails. `dev` is a device index (-1: not CUDA).
+
+def _refuse(where: str, what: str, t=None):
+    got = "" if t is None else f", got {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}"
+    raise ValueError(f"{where}: {what}{got}")
 
 
-def _rows(t, where, name, heads, d, dtype, device):
-    """Token stride (elements) of a [n, heads, d] tensor whose heads are packed; the rest of its layout is refused."""
-    st = t.stride()
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype is not dtype or t.device != device:
-        _refuse(where, f"{name} must be a {dtype} tensor [n, {heads}, {d}] on {device}, got {t.dtype} "
-                       f"{tuple(t.shape)} on {t.device}")
-    if t.shape[0] and (st[2] != 1 or (heads > 1 and st[1] != d)):
-        _refuse(where, f"{name}'s heads must be packed (strides {st})")
-    return st[0] if t.shape[0] > 1 else heads * d
+def _rows(t, where, name, heads, d, dtype, dev):
+    """Token stride (elements) of a [n, heads, d] tensor whose heads are packed; any other layout is refused."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 3 or t.size(1) != heads or t.size(2) != d:
+        _refuse(where, f"{name} must be a {dtype} tensor [n, {heads}, {d}] on device {dev}", t)
+    if t.is_contiguous():
+        return heads * d
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
+        _refuse(where, f"{name}'s heads must be packed", t)
+    return s0 if t.size(0) > 1 else heads * d
 
 
-def _int32(t, where, name, n, device):
-    """An int32 array of at least n entries; None passes."""
-    if t is not None and (t.dtype is not torch.int32 or t.device != device or t.numel() < n or not t.is_contiguous()):
-        _refuse(where, f"{name} must be a contiguous int32 tensor of at least {n} entries on {device}, got {t.dtype} "
-                       f"{tuple(t.shape)} on {t.device}")
-    return None if t is None else t.data_ptr()
-
-
-def _pool(t, where, name, cfg, device):
-    if (t.dtype is not cfg.torch_dtype or t.device != device or not t.is_contiguous()
-            or t.numel() != cfg.n_pages * cfg.n_kv_heads * cfg.page_size * cfg.head_dim):
-        _refuse(where, f"{name} must be a contiguous {cfg.torch_dtype} tensor [{cfg.n_pages}, {cfg.n_kv_heads}, "
-                       f"{cfg.page_size}, {cfg.head_dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _int32(t, where, name, n, dev):
+    """The address of an int32 array of at least n entries; None passes."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous int32 tensor of at least {n} entries on device {dev}", t)
     return t.data_ptr()
 
 
-def _call(where, fn, device, stream, args):
-    """fn(*args, stream) on `device` (made current for the call where it is not), on its current stream by default."""
-    if device.type != "cuda":
-        _refuse(where, f"tensors must be on a CUDA device, got {device}")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+def _block(t, where, name, n, dtype, dev):
+    """The address of a contiguous array of n elements."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous {dtype} tensor of {n} elements on device {dev}", t)
+    return t.data_ptr()
+
+
+def _call(where, fn, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current, on its current stream by default."""
+    if dev < 0:
+        _refuse(where, "tensors must be on a CUDA device")
+    here = torch._C._cuda_getDevice()
+    if dev != here:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
-        code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if code != 0:
         raise ZhaError(code, where)
 
@@ -350,39 +374,41 @@ class Rotary:
         self.freq = torch.tensor(list(table), dtype=torch.float64).to(device)
         self.desc = RotaryDesc(int(rotary_dim), lay.get(layout, layout), m.value, 0, self.freq.data_ptr())
         self.ref = ctypes.byref(self.desc)
+        self.device = self.freq.get_device()
 
 
 def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
     """Rotate q [n, Hq, d] and k [n, Hk, d] (either may be None; tokens may be strided) at int32 positions [n].
     The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out)."""
     where = "zha_rotary_apply"
-    one = q if q is not None else k
-    if one is None:
-        _refuse(where, "q or k is needed")
-    n, d, dt, dev = one.shape[0], one.shape[-1], one.dtype, one.device
-    if dt is not torch.bfloat16 and dt is not torch.float32:
-        _refuse(where, f"dtype {dt} is not supported")
-    args = []
-    heads = []
-    outs = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            heads.append(0)
-            args.append((None, 0, None, 0))
-            outs.append(None)
-            continue
-        y = x if y is None else y
-        if x.dim() != 3 or x.shape[0] != n or y.shape != x.shape:
-            _refuse(where, f"{name} and {name}_out must be [{n}, heads, {d}]")
-        heads.append(x.shape[1])
-        args.append((x.data_ptr(), _rows(x, where, name, x.shape[1], d, dt, dev), y.data_ptr(),
-                     _rows(y, where, name + "_out", x.shape[1], d, dt, dev)))
-        outs.append(y)
-    (qp, qs, qo, qos), (kp, ks, ko, kos) = args
-    _call(where, _lib.zha_rotary_apply, dev, stream,
-          (rot.ref, d, ZHA_BF16 if dt is torch.bfloat16 else ZHA_F32, n, heads[0], heads[1], qp, qs, kp, ks,
-           _int32(positions, where, "positions", n, dev), qo, qos, ko, kos, 1 if transpose else 0))
-    return outs[0], outs[1]
+    one = k if q is None else q
+    if one is None or one.dim() != 3:
+        _refuse(where, "q or k [n, heads, d] is needed", one)
+    n, d, dt, dev = one.size(0), one.size(2), one.dtype, one.get_device()
+    code = _DTYPES.get(dt)
+    if code is None:
+        _refuse(where, "bf16 or fp32 is needed", one)
+    hq = hk = qs = ks = qos = kos = 0
+    qp = kp = qo = ko = None
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        hq = q.size(1)
+        qp, qs = q.data_ptr(), _rows(q, where, "q", hq, d, dt, dev)
+        qo, qos = q_out.data_ptr(), _rows(q_out, where, "q_out", hq, d, dt, dev)
+        if q_out.size(0) != n:
+            _refuse(where, f"q_out must have {n} tokens", q_out)
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        hk = k.size(1) if k.dim() == 3 else 0
+        kp, ks = k.data_ptr(), _rows(k, where, "k", hk, d, dt, dev)
+        ko, kos = k_out.data_ptr(), _rows(k_out, where, "k_out", hk, d, dt, dev)
+        if k.size(0) != n or k_out.size(0) != n:
+            _refuse(where, f"k and k_out must have {n} tokens", k)
+    if rot.device != dev:
+        _refuse(where, f"the rotary table is on device {rot.device}, the tensors on {dev}")
+    _call(where, _lib.zha_rotary_apply, dev, stream, rot.ref, d, code, n, hq, hk, qp, qs, kp, ks,
+          _int32(positions, where, "positions", n, dev), qo, qos, ko, kos, 1 if transpose else 0)
+    return q_out, k_out
 
 
 def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_map, lens_out=None, n_free_out=None,
@@ -390,41 +416,43 @@ def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_m
     """Block tables, slots and lengths of a step with n_new[b] new tokens of sequence b (< 0: it ends).
     token_map: {"positions", "slots", "seq_ids"} (one entry per row of the token buffer) and "cu" [batch + 1];
     lens_out and n_free_out default to lens and n_free (in place)."""
-    where, dev, B = "zha_paged_plan", table.device, cfg.batch
-    rows = token_map["slots"].numel()
-    m = TokenMap(_int32(token_map["positions"], where, "positions", rows, dev),
-                 _int32(token_map["slots"], where, "slots", rows, dev),
+    where, dev, B = "zha_paged_plan", table.get_device(), cfg.batch
+    slots = token_map["slots"]
+    rows = slots.numel()
+    m = TokenMap(_int32(token_map["positions"], where, "positions", rows, dev), _int32(slots, where, "slots", rows, dev),
                  _int32(token_map["seq_ids"], where, "seq_ids", rows, dev),
                  _int32(token_map["cu"], where, "cu", B + 1, dev), rows, 0)
-    _call(where, _lib.zha_paged_plan, dev, stream,
-          (ctypes.byref(cfg), _int32(table, where, "table", B * cfg.max_pages, dev),
-           _int32(lens, where, "lens", B, dev), _int32(n_new, where, "n_new", B, dev),
-           _int32(free_pages, where, "free_pages", cfg.n_pages, dev), _int32(n_free, where, "n_free", 1, dev),
-           _int32(lens if lens_out is None else lens_out, where, "lens_out", B, dev),
-           _int32(n_free if n_free_out is None else n_free_out, where, "n_free_out", 1, dev), ctypes.byref(m),
-           _int32(dev_status, where, "dev_status", 1, dev)))
+    lens_p, free_p = _int32(lens, where, "lens", B, dev), _int32(n_free, where, "n_free", 1, dev)
+    _call(where, _lib.zha_paged_plan, dev, stream, cfg.ref, _int32(table, where, "table", B * cfg.max_pages, dev),
+          lens_p, _int32(n_new, where, "n_new", B, dev), _int32(free_pages, where, "free_pages", cfg.n_pages, dev), free_p,
+          lens_p if lens_out is None else _int32(lens_out, where, "lens_out", B, dev),
+          free_p if n_free_out is None else _int32(n_free_out, where, "n_free_out", 1, dev), ctypes.byref(m),
+          _int32(dev_status, where, "dev_status", 1, dev))
 
 
 def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status=None,
                 stream=None):
     """Rotate q and k_new [n, heads, d] and write k_new, v_new to their cache slots [n] (negative: skipped).
     rot None: no rotation; q None: keys and values only."""
-    where, dev, dt, d = "zha_paged_write", k_pool.device, cfg.torch_dtype, cfg.head_dim
-    n = k_new.shape[0]
-    if v_new.shape[0] != n or (q is not None and (q.shape[0] != n or q_out is None or q_out.shape != q.shape
-                                                  or not q_out.is_contiguous())):
-        _refuse(where, f"q, q_out (contiguous) and v_new must have k_new's {n} tokens")
-    hq, hkv = cfg.n_q_heads, cfg.n_kv_heads
+    where, dev, dt, d, hkv = "zha_paged_write", k_pool.get_device(), cfg.torch_dtype, cfg.head_dim, cfg.n_kv_heads
+    ks, vs, qs, qp, qo = (_rows(k_new, where, "k_new", hkv, d, dt, dev), _rows(v_new, where, "v_new", hkv, d, dt, dev),
+                          0, None, None)
+    n = k_new.size(0)
+    if v_new.size(0) != n:
+        _refuse(where, f"v_new must have k_new's {n} tokens", v_new)
     if q is not None:
-        _rows(q_out, where, "q_out", hq, d, dt, dev)
-    _call(where, _lib.zha_paged_write, dev, stream,
-          (ctypes.byref(cfg), None if rot is None else rot.ref, n, None if q is None else q.data_ptr(),
-           0 if q is None else _rows(q, where, "q", hq, d, dt, dev), k_new.data_ptr(),
-           _rows(k_new, where, "k_new", hkv, d, dt, dev), v_new.data_ptr(),
-           _rows(v_new, where, "v_new", hkv, d, dt, dev), _int32(positions, where, "positions", n, dev),
-           _int32(slots, where, "slots", n, dev), None if q is None else q_out.data_ptr(),
-           _pool(k_pool, where, "k_pool", cfg, dev), _pool(v_pool, where, "v_pool", cfg, dev),
-           _int32(dev_status, where, "dev_status", 1, dev)))
+        hq = cfg.n_q_heads
+        qp, qs = q.data_ptr(), _rows(q, where, "q", hq, d, dt, dev)
+        if q.size(0) != n or q_out is None:
+            _refuse(where, f"q must have k_new's {n} tokens, and q_out is needed with it", q)
+        qo = _block(q_out, where, "q_out", n * hq * d, dt, dev)
+    if rot is not None and rot.device != dev:
+        _refuse(where, f"the rotary table is on device {rot.device}, the tensors on {dev}")
+    size = cfg.pool_elements
+    _call(where, _lib.zha_paged_write, dev, stream, cfg.ref, None if rot is None else rot.ref, n, qp, qs,
+          k_new.data_ptr(), ks, v_new.data_ptr(), vs, _int32(positions, where, "positions", n, dev),
+          _int32(slots, where, "slots", n, dev), qo, _block(k_pool, where, "k_pool", size, dt, dev),
+          _block(v_pool, where, "v_pool", size, dt, dev), _int32(dev_status, where, "dev_status", 1, dev))
     return q_out
 
 
@@ -432,23 +460,22 @@ def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspac
                  positions=None, dev_status=None, stream=None):
     """Attention of rows q [n, Hq, d] over the paged cache into out (and lse [n, Hq] fp32). Row r is of sequence
     seq_ids[r] (default r; negative: left as it is) and attends tokens 0 .. positions[r] (default: all)."""
-    where, dev, dt = "zha_paged_decode", q.device, cfg.torch_dtype
-    n, shape = q.shape[0], (q.shape[0], cfg.n_q_heads, cfg.head_dim)
-    if (q.shape != shape or out.shape != shape or q.dtype is not dt or out.dtype is not dt or out.device != dev
-            or not q.is_contiguous() or not out.is_contiguous()):
-        _refuse(where, f"q and out must be contiguous {dt} tensors {shape} on one device")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2] or lse.device != dev
-                            or not lse.is_contiguous()):
-        _refuse(where, f"lse must be a contiguous fp32 tensor {shape[:2]}")
-    if (workspace.device != dev or not workspace.is_contiguous()
-            or workspace.numel() * workspace.element_size() < _lib.zha_paged_workspace_bytes(ctypes.byref(cfg), n)):
-        _refuse(where, f"the workspace must hold paged_workspace_bytes(cfg, {n}) bytes on {dev}")
-    _call(where, _lib.zha_paged_decode, dev, stream,
-          (ctypes.byref(cfg), n, q.data_ptr(), _pool(k_pool, where, "k_pool", cfg, dev),
-           _pool(v_pool, where, "v_pool", cfg, dev), _int32(table, where, "table", cfg.batch * cfg.max_pages, dev),
-           _int32(lens, where, "lens", cfg.batch, dev), _int32(seq_ids, where, "seq_ids", n, dev),
-           _int32(positions, where, "positions", n, dev), out.data_ptr(), None if lse is None else lse.data_ptr(),
-           workspace.data_ptr(), _int32(dev_status, where, "dev_status", 1, dev)))
+    where, dev, dt, hq, d = "zha_paged_decode", q.get_device(), cfg.torch_dtype, cfg.n_q_heads, cfg.head_dim
+    if _rows(q, where, "q", hq, d, dt, dev) != hq * d or _rows(out, where, "out", hq, d, dt, dev) != hq * d:
+        _refuse(where, "q and out must be contiguous", q)
+    n = q.size(0)
+    if out.size(0) != n:
+        _refuse(where, f"out must have q's {n} rows", out)
+    if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < cfg.decode_workspace(n):
+        _refuse(where, f"the workspace must be contiguous and hold paged_workspace_bytes(cfg, {n}) bytes on device {dev}",
+                workspace)
+    size, batch = cfg.pool_elements, cfg.batch
+    _call(where, _lib.zha_paged_decode, dev, stream, cfg.ref, n, q.data_ptr(),
+          _block(k_pool, where, "k_pool", size, dt, dev), _block(v_pool, where, "v_pool", size, dt, dev),
+          _int32(table, where, "table", batch * cfg.max_pages, dev), _int32(lens, where, "lens", batch, dev),
+          _int32(seq_ids, where, "seq_ids", n, dev), _int32(positions, where, "positions", n, dev), out.data_ptr(),
+          None if lse is None else _block(lse, where, "lse", n * hq, torch.float32, dev), workspace.data_ptr(),
+          _int32(dev_status, where, "dev_status", 1, dev))
     return out
 
 
