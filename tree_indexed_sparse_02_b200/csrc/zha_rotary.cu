@@ -6,34 +6,24 @@
 // Pair (x, y) of a head at position n turns by the angle a = 2 pi n freq:
 //   x' = m (x cos a - y sin a),  y' = m (x sin a + y cos a);
 // the transposed map (the gradient) has the sine's sign flipped.
+//
+// A warp works on one token (or a share of its heads, where tokens are few).
+// A head is NP lanes' work, each with two 16-byte chunks that hold whole
+// pairs, so a lane turns the same coordinates of every head it meets: its
+// cosines and sines stay in registers, formed once per token by the whole warp
+// (one or two per lane, dealt out by shuffles).
 #include "zha_paged.cuh"
 
 namespace zha {
 
 namespace {
 
-constexpr int kThreads = 256;
-
-// n / D for n < 2^16 and D < 2^16 by one multiplication.
-struct Div {
-    uint64_t m;
-    int D;
-    explicit Div(int d = 1) : m(((uint64_t(1) << 32) + d - 1) / d), D(d) {}
-    __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> 32); }
-};
-
-struct Shape {
-    int items_rot;          // items of a q or k head
-    int items_v;            // items of a v head
-    int items_q;            // items of a token's q heads; then k, then v heads
-    int items_qk, items_all;
-    int tok;                // tokens per CTA
-    int per;                // items of each token per CTA (blockIdx.y chooses which)
-    Div by_per, by_rot;
-};
+constexpr int kWarps = 8;                // per CTA
+constexpr int kFillWarps = 148 * 16;     // warps that keep the GPU busy
+constexpr int kDepth = 3;                // heads whose loads a lane has in flight
 
 template <typename T>
-struct Vec {                // 16 bytes
+struct Vec {                             // 16 bytes
     static constexpr int N = 16 / sizeof(T);
     uint4 raw;
     __device__ __forceinline__ void load(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
@@ -60,140 +50,189 @@ __device__ __forceinline__ float2 cos_sin(int n, double f, float m, float sign) 
     return make_float2(m * ((quad == 1 || quad == 2) ? -cc : cc), sign * m * ((quad >= 2) ? -ss : ss));
 }
 
-enum { kHalfVec = 0, kPairVec = 1, kScalar = 2 };
+// The two chunks of a lane, c of NP, and the pairs in them:
+//   kHalf         chunk c of the first half of the rotated part and its
+//                 partner in the second, then chunks that pass through;
+//   kInterleaved  chunks c and c + NP, each of V / 2 whole pairs (also where
+//                 nothing is rotated);
+//   kStaged       the same chunks of a half layout whose halves are not whole
+//                 chunks: the partners come through shared memory.
+enum { kHalf = 0, kInterleaved = 1, kStaged = 2 };
 
-// MODE kHalfVec: an item of a q/k head is a 16-byte chunk of the first half
-// with its partner in the second, or a chunk that passes through;
-// kPairVec (interleaved): a 16-byte chunk; kScalar (half layouts whose halves
-// are not whole chunks): one pair, or one coordinate that passes through.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, Shape sh) {
-    constexpr int V = Vec<T>::N;
-    extern __shared__ float2 cs[];                   // [tok][rd / 2]
-    __shared__ int64_t row[64];                      // cache row of each token, -1: skip
-    const int t0 = blockIdx.x * sh.tok, i0 = blockIdx.y * sh.per;
-    const int nt = min(sh.tok, a.n_tokens - t0), ni = min(sh.per, sh.items_all - i0);
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const __grid_constant__ RotaryArgs a, int share) {
+    constexpr int V = Vec<T>::N, NP = D / (2 * V), HW = 32 / NP;   // HW: heads of a warp at a time
+    constexpr int PL = D / 64;                                      // pairs whose sine a lane forms
+    __shared__ Vec<T> staged[MODE == kStaged ? kWarps : 1][MODE == kStaged ? 64 : 1];
+    __shared__ float2 table[MODE == kStaged ? kWarps : 1][MODE == kStaged ? D / 2 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = lane & (NP - 1), hs = lane / NP;
+    const int job = blockIdx.x * kWarps + warp, t = job / share, part = job - t * share;
+    if (t >= a.n_tokens) return;
     const int half = a.rd >> 1;
     pdl_wait();
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
-        cs[i] = cos_sin(a.positions[t0 + t], a.freq[p], a.mscale, a.sign);
+
+    int64_t row = 0;                     // the token's cache row
+    if (a.slots) {
+        const int s = a.slots[t];
+        if (s >= a.n_slots && lane == 0) set_status(a.status, ZHA_ERR_INVALID_ARG);
+        if (s < 0 || s >= a.n_slots) return;
+        row = ((int64_t)(s >> a.lps) * a.Hk << a.lps) + (s & ((1 << a.lps) - 1));
     }
-    if (a.slots && threadIdx.x < nt) {
-        const int s = a.slots[t0 + threadIdx.x];
-        if (s >= a.n_slots && blockIdx.y == 0) set_status(a.status, ZHA_ERR_INVALID_ARG);
-        row[threadIdx.x] = (s < 0 || s >= a.n_slots)
-                               ? -1
-                               : ((int64_t)(s >> a.lps) * a.Hk << a.lps) + (s & ((1 << a.lps) - 1));
+    // elements of the lane's two chunks in a head: of queries and keys, and of values
+    const int nrot = half / V, va = c * V, vb = (c + NP) * V;
+    int ea = va, eb = vb;
+    if (MODE == kHalf) {
+        ea = c < nrot ? c * V : a.rd + (c - nrot) * V;
+        eb = c < nrot ? half + c * V : a.rd + (c - nrot + NP - nrot) * V;
     }
-    __syncthreads();
-    for (int idx = threadIdx.x; idx < nt * sh.per; idx += kThreads) {
-        const int t = sh.by_per.of(idx), it = idx - t * sh.per + i0;
-        if (it - i0 >= ni) continue;
-        const int64_t tk = t0 + t;
-        const int64_t rw = a.slots ? row[t] : 0;
-        if (rw < 0) continue;
-        if (it >= sh.items_qk) {                     // values: copied
-            const int j = it - sh.items_qk, h = j / sh.items_v, c = j - h * sh.items_v;
-            Vec<T> x;
-            x.load(static_cast<const T *>(a.v) + tk * a.v_stride + h * a.d + c * V);
-            x.store(static_cast<T *>(a.vpool) + (rw + ((int64_t)h << a.lps)) * a.d + c * V);
-            continue;
-        }
-        const bool is_k = it >= sh.items_q;
-        const int j = is_k ? it - sh.items_q : it;
-        const int h = sh.by_rot.of(j), c = j - h * sh.items_rot;
+    // heads hs + HW j, j = part, part + share, ...: queries, then keys, then values
+    const int heads = a.Hq + a.Hk + (a.v ? a.Hk : 0);
+    struct Place {
         const T *src;
         T *dst;
-        if (!is_k) {
-            src = static_cast<const T *>(a.q) + tk * a.q_stride + h * a.d;
-            dst = static_cast<T *>(a.q_out) + tk * a.q_out_stride + h * a.d;
+        int ea, eb;
+        bool rotate;
+    };
+    auto place = [&](int h) {
+        Place p;
+        p.rotate = h < a.Hq + a.Hk;
+        p.ea = p.rotate ? ea : va;
+        p.eb = p.rotate ? eb : vb;
+        if (h < a.Hq) {
+            p.src = static_cast<const T *>(a.q) + t * a.q_stride + h * D;
+            p.dst = static_cast<T *>(a.q_out) + t * a.q_out_stride + h * D;
+        } else if (p.rotate) {
+            h -= a.Hq;
+            p.src = static_cast<const T *>(a.k) + t * a.k_stride + h * D;
+            p.dst = a.slots ? static_cast<T *>(a.kpool) + (row + ((int64_t)h << a.lps)) * D
+                            : static_cast<T *>(a.k_out) + t * a.k_out_stride + h * D;
         } else {
-            src = static_cast<const T *>(a.k) + tk * a.k_stride + h * a.d;
-            dst = a.slots ? static_cast<T *>(a.kpool) + (rw + ((int64_t)h << a.lps)) * a.d
-                          : static_cast<T *>(a.k_out) + tk * a.k_out_stride + h * a.d;
+            h -= a.Hq + a.Hk;
+            p.src = static_cast<const T *>(a.v) + t * a.v_stride + h * D;
+            p.dst = static_cast<T *>(a.vpool) + (row + ((int64_t)h << a.lps)) * D;
         }
-        const float2 *w = cs + t * half;
-        if (MODE == kHalfVec) {
-            const int nrot = half / V;
-            if (c < nrot) {
-                Vec<T> x, y;
-                x.load(src + c * V);
-                y.load(src + half + c * V);
+        return p;
+    };
+
+    Vec<T> x[kDepth], y[kDepth];
+    auto load = [&](int h, Vec<T> &u, Vec<T> &v) {
+        u.raw = v.raw = make_uint4(0, 0, 0, 0);
+        if (h < heads) {
+            const Place p = place(h);
+            u.load(p.src + p.ea);
+            v.load(p.src + p.eb);
+        }
+    };
+    const int step = HW * share;
+    int h0 = hs + HW * part;
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float u = to_f32(x.at()[e]), v = to_f32(y.at()[e]);
-                    turn(u, v, w[c * V + e]);
-                    x.at()[e] = from_f32<T>(u);
-                    y.at()[e] = from_f32<T>(v);
-                }
-                x.store(dst + c * V);
-                y.store(dst + half + c * V);
-            } else {
-                Vec<T> x;
-                x.load(src + a.rd + (c - nrot) * V);
-                x.store(dst + a.rd + (c - nrot) * V);
-            }
-        } else if (MODE == kPairVec) {
-            Vec<T> x;
-            x.load(src + c * V);
+    for (int e = 0; e < kDepth; ++e) load(h0 + e * step, x[e], y[e]);
+
+    // cosines and sines: the warp's lanes form the token's pairs, then each takes those of its chunks
+    float2 cs[V];
+    {
+        float2 mine[PL];
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-                const int p = (c * V + e) >> 1;
-                if (p < half) {
-                    float u = to_f32(x.at()[e]), v = to_f32(x.at()[e + 1]);
-                    turn(u, v, w[p]);
-                    x.at()[e] = from_f32<T>(u);
-                    x.at()[e + 1] = from_f32<T>(v);
-                }
-            }
-            x.store(dst + c * V);
+        for (int e = 0; e < PL; ++e) {
+            const int p = lane * PL + e;
+            mine[e] = p < half ? cos_sin(a.positions[t], a.freq[p], a.mscale, a.sign) : make_float2(1.f, 0.f);
+            if (MODE == kStaged) table[warp][p] = mine[e];
+        }
+        if (MODE == kStaged) {
+            __syncwarp();
         } else {
-            if (c < half) {
-                float u = to_f32(src[c]), v = to_f32(src[half + c]);
-                turn(u, v, w[c]);
-                dst[c] = from_f32<T>(u);
-                dst[half + c] = from_f32<T>(v);
-            } else {
-                dst[half + c] = src[half + c];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int p = MODE == kHalf ? c * V + k : (k < V / 2 ? c * (V / 2) + k : (c + NP) * (V / 2) + k - V / 2);
+                const int from = (p / PL) & 31, e = MODE == kHalf || V / 2 % PL == 0 ? k % PL : p % PL;
+                cs[k].x = __shfl_sync(0xffffffffu, mine[e].x, from);
+                cs[k].y = __shfl_sync(0xffffffffu, mine[e].y, from);
             }
+        }
+    }
+
+    for (; h0 - hs < heads; h0 += kDepth * step) {
+#pragma unroll
+        for (int e = 0; e < kDepth; ++e) {
+            const int h = h0 + e * step;
+            Vec<T> u = x[e], v = y[e];
+            load(h + kDepth * step, x[e], y[e]);
+            if (MODE == kStaged) {
+                __syncwarp();
+                staged[warp][hs * 2 * NP + c] = u;
+                staged[warp][hs * 2 * NP + NP + c] = v;
+                __syncwarp();
+            }
+            if (h >= heads) continue;
+            const Place p = place(h);
+            if (p.rotate) {
+                if (MODE == kHalf) {
+                    if (c < nrot) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) {
+                            float f = to_f32(u.at()[k]), g = to_f32(v.at()[k]);
+                            turn(f, g, cs[k]);
+                            u.at()[k] = from_f32<T>(f);
+                            v.at()[k] = from_f32<T>(g);
+                        }
+                    }
+                } else if (MODE == kInterleaved) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        Vec<T> &w = k < V / 2 ? u : v;
+                        const int i = k < V / 2 ? 2 * k : 2 * k - V;
+                        if ((k < V / 2 ? va : vb) + i >= a.rd) continue;
+                        float f = to_f32(w.at()[i]), g = to_f32(w.at()[i + 1]);
+                        turn(f, g, cs[k]);
+                        w.at()[i] = from_f32<T>(f);
+                        w.at()[i + 1] = from_f32<T>(g);
+                    }
+                } else {
+                    const T *head = reinterpret_cast<const T *>(&staged[warp][hs * 2 * NP]);
+#pragma unroll
+                    for (int k = 0; k < 2 * V; ++k) {
+                        const int i = (k < V ? va : vb - V) + k;
+                        if (i >= a.rd) continue;
+                        const int q = i < half ? i : i - half;
+                        float f = to_f32(head[q]), g = to_f32(head[q + half]);
+                        turn(f, g, table[warp][q]);
+                        (k < V ? u : v).at()[k % V] = from_f32<T>(i < half ? f : g);
+                    }
+                }
+            }
+            u.store(p.dst + p.ea);
+            v.store(p.dst + p.eb);
         }
     }
     // no early trigger: a kernel behind this one may read q_out before its own wait
 }
 
-template <typename T, int MODE>
+template <typename T, int D, int MODE>
 cudaError_t launch_mode(const RotaryArgs &a, cudaStream_t st) {
-    constexpr int V = Vec<T>::N;
-    Shape sh;
-    const int half = a.rd / 2;
-    sh.items_rot = MODE == kHalfVec ? half / V + (a.d - a.rd) / V : MODE == kPairVec ? a.d / V : half + (a.d - a.rd);
-    sh.items_v = a.d / V;
-    sh.items_q = a.Hq * sh.items_rot;
-    sh.items_qk = sh.items_q + a.Hk * sh.items_rot;
-    sh.items_all = sh.items_qk + (a.v ? a.Hk * sh.items_v : 0);
-    sh.per = sh.items_all < 1024 ? sh.items_all : 1024;
-    sh.tok = 1024 / sh.per;
-    if (sh.tok > 16) sh.tok = 16;
-    sh.by_per = Div(sh.per);
-    sh.by_rot = Div(sh.items_rot);
-    const dim3 grid((a.n_tokens + sh.tok - 1) / sh.tok, (sh.items_all + sh.per - 1) / sh.per);
+    constexpr int HW = 32 / (D / (2 * Vec<T>::N));
+    // warps per token: one where tokens alone fill the GPU, more where they do not, up to one for each HW heads
+    const int most = (a.Hq + a.Hk + (a.v ? a.Hk : 0) + HW - 1) / HW, want = kFillWarps / a.n_tokens;
+    const int share = want < 1 ? 1 : want > most ? most : want;
+    const int64_t jobs = (int64_t)a.n_tokens * share;
+    if (jobs > INT32_MAX - kWarps) return cudaErrorInvalidValue;
     ProfScope ps(a.slots ? "paged_write" : "rotary", st);
-    return launch_pdl(rotary_kernel<T, MODE>, grid, dim3(kThreads), sizeof(float2) * sh.tok * (half ? half : 1), st, a, sh);
+    return launch_pdl(rotary_kernel<T, D, MODE>, dim3((unsigned)((jobs + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, a, share);
 }
 
-template <typename T>
-cudaError_t launch_type(const RotaryArgs &a, cudaStream_t st) {
-    constexpr int V = Vec<T>::N;
-    if (a.rd == 0 || a.layout == ZHA_ROPE_INTERLEAVED) return launch_mode<T, kPairVec>(a, st);
-    if ((a.rd / 2) % V == 0) return launch_mode<T, kHalfVec>(a, st);
-    return launch_mode<T, kScalar>(a, st);
+template <typename T, int D>
+cudaError_t launch_dim(const RotaryArgs &a, cudaStream_t st) {
+    if (a.rd == 0 || a.layout == ZHA_ROPE_INTERLEAVED) return launch_mode<T, D, kInterleaved>(a, st);
+    if ((a.rd / 2) % Vec<T>::N == 0) return launch_mode<T, D, kHalf>(a, st);
+    return launch_mode<T, D, kStaged>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t st) {
-    return a.dtype == ZHA_BF16 ? launch_type<__nv_bfloat16>(a, st) : launch_type<float>(a, st);
+    if (a.dtype == ZHA_BF16)
+        return a.d == 128 ? launch_dim<__nv_bfloat16, 128>(a, st) : launch_dim<__nv_bfloat16, 64>(a, st);
+    return a.d == 128 ? launch_dim<float, 128>(a, st) : launch_dim<float, 64>(a, st);
 }
 
 }  // namespace zha
