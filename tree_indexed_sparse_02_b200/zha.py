@@ -151,6 +151,8 @@ def _load():
 
 
 _lib = _load()
+_rotary_apply, _paged_plan = _lib.zha_rotary_apply, _lib.zha_paged_plan
+_paged_write, _paged_decode = _lib.zha_paged_write, _lib.zha_paged_decode
 
 
 def lib():
@@ -315,16 +317,15 @@ def _refuse(where: str, what: str, t=None):
     raise ValueError(f"{where}: {what}{got}")
 
 
-def _rows(t, where, name, heads, d, dtype, dev):
-    """Token stride (elements) of a [n, heads, d] tensor whose heads are packed; any other layout is refused."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 3 or t.size(1) != heads or t.size(2) != d:
-        _refuse(where, f"{name} must be a {dtype} tensor [n, {heads}, {d}] on device {dev}", t)
-    if t.is_contiguous():
-        return heads * d
+def _rows(t, where, name, n, heads, d, dtype, dev):
+    """The address and the token stride (elements) of a [n, heads, d] tensor whose heads are packed; any other layout
+    is refused."""
+    if t.shape != (n, heads, d) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(where, f"{name} must be a {dtype} tensor [{n}, {heads}, {d}] on device {dev}", t)
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != d):
+    if (s2 != 1 or (s1 != d and heads > 1)) and n > 0:
         _refuse(where, f"{name}'s heads must be packed", t)
-    return s0 if t.size(0) > 1 else heads * d
+    return t.data_ptr(), s0 if n > 1 else heads * d
 
 
 def _int32(t, where, name, n, dev):
@@ -382,31 +383,31 @@ def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False
     The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out)."""
     where = "zha_rotary_apply"
     one = k if q is None else q
-    if one is None or one.dim() != 3:
+    if one is None or one.ndim != 3:
         _refuse(where, "q or k [n, heads, d] is needed", one)
-    n, d, dt, dev = one.size(0), one.size(2), one.dtype, one.get_device()
+    (n, heads, d), dt, dev = one.shape, one.dtype, one.get_device()
     code = _DTYPES.get(dt)
     if code is None:
         _refuse(where, "bf16 or fp32 is needed", one)
     hq = hk = qs = ks = qos = kos = 0
     qp = kp = qo = ko = None
     if q is not None:
-        q_out = q if q_out is None else q_out
-        hq = q.size(1)
-        qp, qs = q.data_ptr(), _rows(q, where, "q", hq, d, dt, dev)
-        qo, qos = q_out.data_ptr(), _rows(q_out, where, "q_out", hq, d, dt, dev)
-        if q_out.size(0) != n:
-            _refuse(where, f"q_out must have {n} tokens", q_out)
+        hq = heads
+        qp, qs = _rows(q, where, "q", n, hq, d, dt, dev)
+        if q_out is None:
+            q_out, qo, qos = q, qp, qs
+        else:
+            qo, qos = _rows(q_out, where, "q_out", n, hq, d, dt, dev)
     if k is not None:
-        k_out = k if k_out is None else k_out
-        hk = k.size(1) if k.dim() == 3 else 0
-        kp, ks = k.data_ptr(), _rows(k, where, "k", hk, d, dt, dev)
-        ko, kos = k_out.data_ptr(), _rows(k_out, where, "k_out", hk, d, dt, dev)
-        if k.size(0) != n or k_out.size(0) != n:
-            _refuse(where, f"k and k_out must have {n} tokens", k)
+        hk = k.shape[1] if k.ndim == 3 else 0
+        kp, ks = _rows(k, where, "k", n, hk, d, dt, dev)
+        if k_out is None:
+            k_out, ko, kos = k, kp, ks
+        else:
+            ko, kos = _rows(k_out, where, "k_out", n, hk, d, dt, dev)
     if rot.device != dev:
         _refuse(where, f"the rotary table is on device {rot.device}, the tensors on {dev}")
-    _call(where, _lib.zha_rotary_apply, dev, stream, rot.ref, d, code, n, hq, hk, qp, qs, kp, ks,
+    _call(where, _rotary_apply, dev, stream, rot.ref, d, code, n, hq, hk, qp, qs, kp, ks,
           _int32(positions, where, "positions", n, dev), qo, qos, ko, kos, 1 if transpose else 0)
     return q_out, k_out
 
@@ -423,7 +424,7 @@ def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_m
                  _int32(token_map["seq_ids"], where, "seq_ids", rows, dev),
                  _int32(token_map["cu"], where, "cu", B + 1, dev), rows, 0)
     lens_p, free_p = _int32(lens, where, "lens", B, dev), _int32(n_free, where, "n_free", 1, dev)
-    _call(where, _lib.zha_paged_plan, dev, stream, cfg.ref, _int32(table, where, "table", B * cfg.max_pages, dev),
+    _call(where, _paged_plan, dev, stream, cfg.ref, _int32(table, where, "table", B * cfg.max_pages, dev),
           lens_p, _int32(n_new, where, "n_new", B, dev), _int32(free_pages, where, "free_pages", cfg.n_pages, dev), free_p,
           lens_p if lens_out is None else _int32(lens_out, where, "lens_out", B, dev),
           free_p if n_free_out is None else _int32(n_free_out, where, "n_free_out", 1, dev), ctypes.byref(m),
@@ -435,24 +436,23 @@ def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out,
     """Rotate q and k_new [n, heads, d] and write k_new, v_new to their cache slots [n] (negative: skipped).
     rot None: no rotation; q None: keys and values only."""
     where, dev, dt, d, hkv = "zha_paged_write", k_pool.get_device(), cfg.torch_dtype, cfg.head_dim, cfg.n_kv_heads
-    ks, vs, qs, qp, qo = (_rows(k_new, where, "k_new", hkv, d, dt, dev), _rows(v_new, where, "v_new", hkv, d, dt, dev),
-                          0, None, None)
-    n = k_new.size(0)
-    if v_new.size(0) != n:
-        _refuse(where, f"v_new must have k_new's {n} tokens", v_new)
+    n = k_new.shape[0]
+    kp, ks = _rows(k_new, where, "k_new", n, hkv, d, dt, dev)
+    vp, vs = _rows(v_new, where, "v_new", n, hkv, d, dt, dev)
+    qs, qp, qo = 0, None, None
     if q is not None:
         hq = cfg.n_q_heads
-        qp, qs = q.data_ptr(), _rows(q, where, "q", hq, d, dt, dev)
-        if q.size(0) != n or q_out is None:
-            _refuse(where, f"q must have k_new's {n} tokens, and q_out is needed with it", q)
+        qp, qs = _rows(q, where, "q", n, hq, d, dt, dev)
+        if q_out is None:
+            _refuse(where, "q_out is needed with q")
         qo = _block(q_out, where, "q_out", n * hq * d, dt, dev)
     if rot is not None and rot.device != dev:
         _refuse(where, f"the rotary table is on device {rot.device}, the tensors on {dev}")
     size = cfg.pool_elements
-    _call(where, _lib.zha_paged_write, dev, stream, cfg.ref, None if rot is None else rot.ref, n, qp, qs,
-          k_new.data_ptr(), ks, v_new.data_ptr(), vs, _int32(positions, where, "positions", n, dev),
-          _int32(slots, where, "slots", n, dev), qo, _block(k_pool, where, "k_pool", size, dt, dev),
-          _block(v_pool, where, "v_pool", size, dt, dev), _int32(dev_status, where, "dev_status", 1, dev))
+    _call(where, _paged_write, dev, stream, cfg.ref, None if rot is None else rot.ref, n, qp, qs, kp, ks, vp, vs,
+          _int32(positions, where, "positions", n, dev), _int32(slots, where, "slots", n, dev), qo,
+          _block(k_pool, where, "k_pool", size, dt, dev), _block(v_pool, where, "v_pool", size, dt, dev),
+          _int32(dev_status, where, "dev_status", 1, dev))
     return q_out
 
 
@@ -461,19 +461,17 @@ def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspac
     """Attention of rows q [n, Hq, d] over the paged cache into out (and lse [n, Hq] fp32). Row r is of sequence
     seq_ids[r] (default r; negative: left as it is) and attends tokens 0 .. positions[r] (default: all)."""
     where, dev, dt, hq, d = "zha_paged_decode", q.get_device(), cfg.torch_dtype, cfg.n_q_heads, cfg.head_dim
-    if _rows(q, where, "q", hq, d, dt, dev) != hq * d or _rows(out, where, "out", hq, d, dt, dev) != hq * d:
-        _refuse(where, "q and out must be contiguous", q)
-    n = q.size(0)
-    if out.size(0) != n:
-        _refuse(where, f"out must have q's {n} rows", out)
+    n, size, batch = q.shape[0], cfg.pool_elements, cfg.batch
+    if q.ndim != 3 or (seq_ids is None and n > batch):
+        _refuse(where, f"q must be [n, {hq}, {d}] with a sequence for each row", q)
+    qp, op = _block(q, where, "q", n * hq * d, dt, dev), _block(out, where, "out", n * hq * d, dt, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < cfg.decode_workspace(n):
         _refuse(where, f"the workspace must be contiguous and hold paged_workspace_bytes(cfg, {n}) bytes on device {dev}",
                 workspace)
-    size, batch = cfg.pool_elements, cfg.batch
-    _call(where, _lib.zha_paged_decode, dev, stream, cfg.ref, n, q.data_ptr(),
+    _call(where, _paged_decode, dev, stream, cfg.ref, n, qp,
           _block(k_pool, where, "k_pool", size, dt, dev), _block(v_pool, where, "v_pool", size, dt, dev),
           _int32(table, where, "table", batch * cfg.max_pages, dev), _int32(lens, where, "lens", batch, dev),
-          _int32(seq_ids, where, "seq_ids", n, dev), _int32(positions, where, "positions", n, dev), out.data_ptr(),
+          _int32(seq_ids, where, "seq_ids", n, dev), _int32(positions, where, "positions", n, dev), op,
           None if lse is None else _block(lse, where, "lse", n * hq, torch.float32, dev), workspace.data_ptr(),
           _int32(dev_status, where, "dev_status", 1, dev))
     return out
