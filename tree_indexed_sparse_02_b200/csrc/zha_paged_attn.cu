@@ -90,17 +90,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// x = hi + lo, each with tf32's 11 significant bits: hi cut off, the rest (13 bits) rounded, so that 2^-22 of x
-// is lost at most. NaN and infinity stay in hi.
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
-}
 // NaN if either is NaN
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
@@ -111,11 +100,6 @@ __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
     return r;
-}
-// main + corr, or main alone where the correction is not finite: the small
-// parts of a split operand would turn an infinite factor into NaN.
-__device__ __forceinline__ float with_correction(float main, float corr) {
-    return fabsf(corr) <= 3.0e38f ? main + corr : main;
 }
 // barriers of the four computing warps (the copying warp takes no part)
 __device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
@@ -156,27 +140,50 @@ struct Tile {
 // not attended
 enum { kFirst = 1, kLast = 2, kHead = 4, kTail = 8, kEdge = 16 };
 
-template <typename T, int D>
+// GP: query heads of a group, padded (fp32: 8 or 16; the bf16 MMA always has 16 rows).
+template <typename T, int D, int GP>
 struct Shared {
+    static constexpr bool kBf16 = sizeof(T) == 2;
     static constexpr int TT = kTileBytes / (D * (int)sizeof(T));   // tokens of a tile
-    static constexpr int PS = TT + 8;    // a row of P, padded against bank conflicts
-    // K then V of a tile: blocks of 8 tokens, [D * sizeof(T) / 128][8][128 bytes], 16-byte chunks
-    // XOR-swizzled by the row (the 128-byte swizzle of a TMA copy)
+    static constexpr int ROWB = D * (int)sizeof(T), CH = ROWB / 16;       // bytes and 16-byte chunks of a row
+    // K then V of a tile: blocks of 8 tokens, [ROWB / 128][8][128 bytes], 16-byte chunks XOR-swizzled by the row
+    // (the 128-byte swizzle of a TMA copy)
     uint8_t ring[kStages][2 * kTileBytes];
-    // P in two parts: weights keep 16 (bf16) or 22 (tf32) bits; one bf16 part alone would cost half an
-    // ulp of the output
-    typedef typename std::conditional<sizeof(T) == 2, __nv_bfloat16, float>::type PT;
-    alignas(16) PT p[2][kRows][PS];
-    static constexpr int QROW = D * (int)sizeof(T) + 16;           // padded: no bank twice
-    static constexpr int QS = sizeof(T) == 2 ? 2 : 1;              // places for the queries of a piece
-    alignas(16) uint8_t q[QS][kRows][QROW];
+    // The weights. bf16: as MMA operand rows [head][token], in two parts (16 bits; one bf16 part alone would cost
+    // half an ulp of the output), padded against bank conflicts; fp32: [token][head].
+    typedef typename std::conditional<kBf16, __nv_bfloat16[2][kRows][TT + 8], float[TT][kRows]>::type Weights;
+    alignas(16) Weights p;
+    // the queries of a piece, in one of QS places; bf16 rows are padded (read as fragments: no bank twice)
+    static constexpr int QROW = ROWB + (kBf16 ? 16 : 0), QS = kBf16 || GP == 8 ? 2 : 1;
+    alignas(16) uint8_t q[QS][kBf16 ? kRows : GP][QROW];
     Tile tile[kStages];
+    alignas(16) float corr[kRows];
     float mx[kWarps][kRows], sum[kWarps][kRows];
-    int scan[kThreads / 32];
     // of the rows that this part's two ends fall into: the row, tiles before it, its own tiles (of each head)
     int edge_row[2], edge_before[2], edge_tiles[2];
+    int scan[kThreads / 32];
     uint64_t full[kStages], empty[kStages], q_empty[QS];
     int last, abort;
+
+    // byte offset of a token's 16-byte chunk in K or V of a tile
+    static __device__ __forceinline__ int at(int t, int ch) {
+        return (t >> 3) * 8 * ROWB + (ch >> 3) * 1024 + (t & 7) * 128 + (((ch & 7) ^ (t & 7)) << 4);
+    }
+    // token t of the tile in stage st is outside the row's range or on no page
+    __device__ __forceinline__ bool hidden(const Tile &d, int st, int t) const {
+        const int pos = d.base + t;
+        return pos < d.lo || pos >= d.hi || ((tile[st].bad[t >> 5] >> (t & 31)) & 1u);
+    }
+    // clears this warp's coordinates of the hidden tokens' value rows, which no other warp reads (their weights are
+    // 0, but 0 times what the rows hold can be NaN)
+    __device__ __forceinline__ void clear_hidden(const Tile &d, int st, int warp, int lane) {
+        for (int i = lane; i < TT * CH / 4; i += 32) {
+            const int t = i / (CH / 4), ch = warp * (CH / 4) + i % (CH / 4);
+            if (hidden(d, st, t)) *reinterpret_cast<uint4 *>(ring[st] + kTileBytes + at(t, ch)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();          // before a later copy lands there
+        __syncwarp();
+    }
 };
 
 // Joins cnt pieces in slots s0, s1, s1 + step, ... of the workspace, eight at a time; the result goes to the
@@ -241,16 +248,538 @@ __device__ __forceinline__ void join(const PagedAttnArgs &a, float *parts, int c
     }
 }
 
-template <typename T, int D, bool kTma>
+// Announces this CTA's piece (or set of pieces) at a counter; true in the CTA that is the last of `of`. (The
+// barrier puts every thread's stores before thread 0's fence, which publishes them; the pieces are read past L1.)
+__device__ __forceinline__ bool arrive(int32_t *counter, int of, int &sm_last) {
+    math_sync();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        const bool last = atomicAdd(counter, 1) == of - 1;
+        if (last) {
+            __threadfence();
+            *counter = 0;
+        }
+        sm_last = last;
+    }
+    math_sync();
+    return sm_last != 0;
+}
+
+// The last piece of a group to arrive joins them all; with many pieces the last of a set of about sqrt(pieces)
+// joins the set into its first piece's place, and the last set to arrive joins the sets.
+template <typename T, int D>
+__device__ __forceinline__ void join_group(const PagedAttnArgs &a, float *parts, int32_t *arrived, const Tile &d, int64_t head,
+                                           int &sm_last) {
+    const int pieces = d.pieces, slot0 = 2 * d.c_first + 1, mine = (int)blockIdx.x - d.c_first;
+    int set = pieces;
+    if (pieces > kDirect) {
+        set = kDirect / 2;
+        while (set * set < pieces) ++set;
+    }
+    const int i0 = mine / set * set, in_set = min(set, pieces - i0), sets = (pieces + set - 1) / set;
+    const int set0 = i0 == 0 ? slot0 : 2 * (d.c_first + i0);
+    int32_t *counter = arrived + set0;
+    int cnt = in_set, s0 = set0, s1 = 2 * (d.c_first + i0 + 1), step = 2;
+    bool back = sets > 1;
+#pragma unroll 1
+    while (arrive(counter, cnt, sm_last)) {
+        join<T, D>(a, parts, cnt, s0, s1, step, head, back);
+        if (!back) break;
+        counter = arrived + 2 * kMaxWorkers + slot0;       // now the sets
+        cnt = sets;
+        s0 = slot0;
+        s1 = 2 * (d.c_first + set);
+        step = 2 * set;
+        back = false;
+    }
+}
+
+// This CTA's place for its piece of a split group (null: the piece is the group): slot 2c + 1 for a group's first
+// piece, 2c for another.
+__device__ __forceinline__ float *piece_place(const PagedAttnArgs &a, float *parts, int flags) {
+    if ((flags & (kHead | kTail)) == (kHead | kTail)) return nullptr;
+    return parts + (2 * (int64_t)blockIdx.x + (flags & kHead ? 1 : 0)) * piece_floats(a.G, a.d);
+}
+
+// bf16: S and O on tensor cores, m16n8k16 with the heads as rows.
+template <int D>
+__device__ __forceinline__ void math_bf16(const PagedAttnArgs &a, Shared<__nv_bfloat16, D, kRows> &sm, float *parts,
+                                          int32_t *arrived, int n) {
+    using T = __nv_bfloat16;
+    using S = Shared<T, D, kRows>;
+    constexpr int TT = S::TT, ROWB = S::ROWB;
+    constexpr int NT = TT / 32;              // 8-token columns of S per warp
+    constexpr int NJ = D / 32;               // 8-wide columns of O per warp
+    constexpr int KS = D / 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gq = lane >> 2, t4 = lane & 3;
+    volatile int *abort = &sm.abort;
+    uint32_t qf[KS][4];                      // Q fragments
+    float o[NJ][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    const float s2 = a.s * kLog2e;
+    const int tok0 = warp * (TT / 4);
+    // byte offsets of this lane's reads of K (two values of bit 2 of the chunk) and of V
+    uint32_t ko[2], vo[NJ / 2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) ko[b] = S::at(tok0 + (lane & 7), 4 * b + (lane >> 3));
+#pragma unroll
+    for (int jp = 0; jp < NJ / 2; ++jp) vo[jp] = S::at(lane & 15, warp * (D / 32) + 2 * jp + (lane >> 4));
+
+    int seg = -1;
+    for (int it = 0; it < n; ++it) {
+        const int st = it % kStages;
+        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
+        const Tile d = sm.tile[st];
+        if (d.flags & kFirst) {
+            ++seg;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int h = gq + 8 * half;
+                const uint32_t *row = reinterpret_cast<const uint32_t *>(sm.q[seg % S::QS][h]);
+#pragma unroll
+                for (int st = 0; st < KS; ++st) {
+                    qf[st][half] = h < a.G ? row[st * 8 + t4] : 0u;
+                    qf[st][2 + half] = h < a.G ? row[st * 8 + 4 + t4] : 0u;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[seg % S::QS]));
+        }
+        const uint32_t kt = smem_u32(sm.ring[st]), vt = kt + kTileBytes;
+
+        // ---- S = Q K^T of this warp's tokens
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kp = 0; kp < D / 32; ++kp) {
+                uint32_t b[4];
+                ldsm4(kt + ko[kp & 1] + nt * 8 * ROWB + (kp >> 1) * 1024, b);
+                mma_bf16(s0, qf[2 * kp], b[0], b[1]);
+                mma_bf16(s1, qf[2 * kp + 1], b[2], b[3]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[nt][u] = (s0[u] + s1[u]) * s2;
+        }
+        if (d.flags & kEdge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (sm.hidden(d, st, tok0 + nt * 8 + 2 * t4 + (u & 1))) x[nt][u] = -INFINITY;
+        }
+        // ---- row maxima over the tile
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mx = max_nan(mx, max_nan(x[nt][2 * r], x[nt][2 * r + 1]));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            if (t4 == 0) sm.mx[warp][gq + 8 * r] = mx;
+        }
+        if (math_any(!ok)) break;          // a wait ran out: every warp leaves here
+        float corr[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float mx = m_run[r];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = max_nan(mx, sm.mx[w][gq + 8 * r]);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            corr[r] = ex2(m_run[r] - ref);
+            m_run[r] = mx;
+            float ls = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float p0 = ex2(x[nt][2 * r] - ref), p1 = ex2(x[nt][2 * r + 1] - ref);
+                ls += p0 + p1;
+                const int at = tok0 + nt * 8 + 2 * t4, h = gq + 8 * r;
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                const float2 hf = __bfloat1622float2(hi);
+                *reinterpret_cast<__nv_bfloat162 *>(&sm.p[0][h][at]) = hi;
+                *reinterpret_cast<__nv_bfloat162 *>(&sm.p[1][h][at]) = __floats2bfloat162_rn(p0 - hf.x, p1 - hf.y);
+            }
+            l_run[r] = l_run[r] * corr[r] + ls;
+        }
+        math_sync();
+        // ---- the tile's P V in accumulators of its own (the MMA truncates its sums: kept short), then into O
+        float pv[NJ][4];
+        auto weigh = [&](bool low) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) pv[j][0] = pv[j][1] = pv[j][2] = pv[j][3] = 0.f;
+#pragma unroll
+            for (int kp = 0; kp < TT / 16; ++kp) {
+                uint32_t ph[4], pl[4];
+                const int prow = lane & 15, pcol = kp * 16 + (lane >> 4) * 8;
+                ldsm4(smem_u32(&sm.p[0][prow][pcol]), ph);
+                if (low) ldsm4(smem_u32(&sm.p[1][prow][pcol]), pl);
+#pragma unroll
+                for (int jp = 0; jp < NJ / 2; ++jp) {
+                    uint32_t b[4];
+                    ldsm4t(vt + vo[jp] + kp * 16 * ROWB, b);
+                    mma_bf16(pv[2 * jp], ph, b[0], b[1]);
+                    mma_bf16(pv[2 * jp + 1], ph, b[2], b[3]);
+                    if (low) {
+                        mma_bf16(pv[2 * jp], pl, b[0], b[1]);
+                        mma_bf16(pv[2 * jp + 1], pl, b[2], b[3]);
+                    }
+                }
+            }
+        };
+        auto finite = [&]() {
+            float odd = 0.f;               // stays 0 if everything is
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) odd = fmaf(pv[j][u], 0.f, odd);
+            return !__any_sync(0xffffffffu, odd != 0.f);
+        };
+        weigh(true);
+        if (!finite()) {
+            // What hidden tokens' value rows hold came in: clear them and do the tile again. An attended infinite
+            // value times a low part can be NaN where the product is infinite: what is not finite then is taken
+            // from the high parts.
+            if (d.flags & kEdge) sm.clear_hidden(d, st, warp, lane);
+            weigh(true);
+            if (!finite()) {
+                float both[NJ][4];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) both[j][u] = pv[j][u];
+                weigh(false);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) pv[j][u] = fabsf(both[j][u]) <= 3.0e38f ? both[j][u] : pv[j][u];
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[j][u] = fmaf(o[j][u], corr[u >> 1], pv[j][u]);
+
+        if (!(d.flags & kLast)) continue;
+        // ---- the end of this CTA's piece of the group: the sums of the warps
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float l = l_run[r];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if (t4 == 0) sm.sum[warp][gq + 8 * r] = l;
+        }
+        math_sync();
+        const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
+        float *part = piece_place(a, parts, d.flags);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) L += sm.sum[w][gq + 8 * r];
+            const int h = gq + 8 * r;
+            if (h < a.G) {
+                if (part) {
+                    if (warp == 0 && t4 == 0) reinterpret_cast<float2 *>(part)[h] = make_float2(m_run[r], L);
+                } else if (a.lse && warp == 0 && t4 == 0) {
+                    a.lse[head + h] = L == 0.f ? -INFINITY : (m_run[r] + log2f(L)) * kLn2;
+                }
+                const float inv = part ? 1.f : L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const float y[2] = {o[j][2 * r] * inv, o[j][2 * r + 1] * inv};
+                    const int at = h * D + warp * (D / 4) + 8 * j + 2 * t4;
+                    if (part) store_vec<2>(part + piece_ml(a.G) + at, y);
+                    else store_vec<2>(static_cast<T *>(a.out) + head * D + at, y);
+                }
+            }
+            m_run[r] = -INFINITY;
+            l_run[r] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        if (part) join_group<T, D>(a, parts, arrived, d, head, sm.last);
+    }
+}
+
+// Two fp32 products and sums at once.
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+struct Four {                                // 16 bytes: four floats as two pairs
+    uint64_t a, b;
+};
+__device__ __forceinline__ Four load4(const void *p) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+    return Four{v.x, v.y};
+}
+
+// fp32, on the CUDA cores two lanes wide (fma.rn.f32x2): products and sums keep fp32's precision, which tensor
+// cores reach only with three or more passes over split operands.
+//   S: 16 lanes share a token's coordinates (a chunk or two each) and take TC tokens and 8 heads at a time; the 16
+//      partial sums are exchanged so that a lane ends with one head's scores of TC / 2 tokens.
+//   O: a lane has 4 coordinates of all heads for every NG-th token; the NG parts meet at the end of the piece.
+template <int D, int GP>
+__device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D, GP> &sm, float *parts, int32_t *arrived,
+                                         int n) {
+    using S = Shared<float, D, GP>;
+    constexpr int TT = S::TT;
+    constexpr int WT = TT / 4;               // tokens of a warp
+    constexpr int CL = D / 64;               // chunks of a lane in S
+    constexpr int TC = GP == 8 ? 4 : 2;      // tokens of a lane at a time (registers)
+    constexpr int NC = WT / (2 * TC);        // times
+    constexpr int NO = GP / 8;               // octets of heads
+    constexpr int NX = NC * TC / 2;          // scores a lane ends with, for each octet
+    constexpr int CW = D / 16;               // chunks of a warp in O: lanes side by side
+    constexpr int NG = 32 / CW;              // groups of lanes, by token
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int dq = lane & 15, ts = lane >> 4, hd = lane & 7, th = (lane >> 3) & 1;
+    const int oc = lane % CW, og = lane / CW;
+    const int tok0 = warp * WT;
+    volatile int *abort = &sm.abort;
+    uint64_t o[GP][2];
+    float m_run[NO], l_run[NO];
+#pragma unroll
+    for (int h = 0; h < GP; ++h) o[h][0] = o[h][1] = 0ull;
+#pragma unroll
+    for (int e = 0; e < NO; ++e) {
+        m_run[e] = -INFINITY;
+        l_run[e] = 0.f;
+    }
+    const float s2 = a.s * kLog2e;
+    // token of score e of a lane
+    auto tok_of = [&](int e) { return tok0 + ts + 2 * ((e / (TC / 2)) * TC + th * (TC / 2) + e % (TC / 2)); };
+
+    int seg = -1;
+    for (int it = 0; it < n; ++it) {
+        const int st = it % kStages;
+        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
+        const Tile d = sm.tile[st];
+        if (d.flags & kFirst) ++seg;
+        const uint8_t *kt = sm.ring[st], *vt = kt + kTileBytes, *qp = sm.q[seg % S::QS][0];
+
+        // ---- S
+        float x[NO][NX];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            Four k[TC][CL];
+#pragma unroll
+            for (int i = 0; i < TC; ++i)
+#pragma unroll
+                for (int j = 0; j < CL; ++j) k[i][j] = load4(kt + S::at(tok0 + ts + 2 * (c * TC + i), dq + 16 * j));
+#pragma unroll
+            for (int e = 0; e < NO; ++e) {
+                float v[TC][8];
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    // (heads beyond the group repeat its last one; their results are dropped)
+                    const uint8_t *row = qp + min(8 * e + h, a.G - 1) * S::QROW;
+                    Four q[CL];
+#pragma unroll
+                    for (int j = 0; j < CL; ++j) q[j] = load4(row + (dq + 16 * j) * 16);
+#pragma unroll
+                    for (int i = 0; i < TC; ++i) {
+                        uint64_t acc = 0ull;
+#pragma unroll
+                        for (int j = 0; j < CL; ++j) {
+                            acc = fma2(k[i][j].a, q[j].a, acc);
+                            acc = fma2(k[i][j].b, q[j].b, acc);
+                        }
+                        const float2 f = unpack2(acc);
+                        v[i][h] = f.x + f.y;
+                    }
+                }
+                // sums over the 16 lanes: by halves of the tokens, then of the heads
+                float w[TC / 2][8], u[TC / 2][4], y[TC / 2][2];
+#pragma unroll
+                for (int i = 0; i < TC / 2; ++i) {
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        const float keep = th ? v[i + TC / 2][h] : v[i][h], give = th ? v[i][h] : v[i + TC / 2][h];
+                        w[i][h] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const bool up = lane & 4;
+                        const float keep = up ? w[i][h + 4] : w[i][h], give = up ? w[i][h] : w[i][h + 4];
+                        u[i][h] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool up = lane & 2;
+                        const float keep = up ? u[i][h + 2] : u[i][h], give = up ? u[i][h] : u[i][h + 2];
+                        y[i][h] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                    }
+                    const bool up = lane & 1;
+                    const float keep = up ? y[i][1] : y[i][0], give = up ? y[i][0] : y[i][1];
+                    x[e][c * (TC / 2) + i] = (keep + __shfl_xor_sync(0xffffffffu, give, 1)) * s2;
+                }
+            }
+        }
+        if (d.flags & kEdge) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                if (sm.hidden(d, st, tok_of(i))) {
+#pragma unroll
+                    for (int e = 0; e < NO; ++e) x[e][i] = -INFINITY;
+                }
+            sm.clear_hidden(d, st, warp, lane);
+        }
+        // ---- maxima over the tile
+#pragma unroll
+        for (int e = 0; e < NO; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NX; ++i) mx = max_nan(mx, x[e][i]);
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (lane < 8) sm.mx[warp][8 * e + lane] = mx;
+        }
+        if (math_any(!ok)) break;          // a wait ran out: every warp leaves here
+#pragma unroll
+        for (int e = 0; e < NO; ++e) {
+            const int h = 8 * e + hd;
+            float mx = m_run[e];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = max_nan(mx, sm.mx[w][h]);
+            const float ref = mx == -INFINITY ? 0.f : mx, corr = ex2(m_run[e] - ref);
+            m_run[e] = mx;
+            float ls = 0.f;
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const float p = ex2(x[e][i] - ref);
+                ls += p;
+                sm.p[tok_of(i)][h] = p;
+            }
+            l_run[e] = l_run[e] * corr + ls;
+            if (tid < 8) sm.corr[h] = corr;
+        }
+        math_sync();
+        // ---- O
+#pragma unroll
+        for (int h = 0; h < GP; h += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(&sm.corr[h]);
+            const float cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint64_t c2 = pack2(cc[u], cc[u]);
+                o[h + u][0] = fma2(o[h + u][0], c2, 0ull);
+                o[h + u][1] = fma2(o[h + u][1], c2, 0ull);
+            }
+        }
+#pragma unroll(GP == 8 ? 4 : 1)
+        for (int i = 0; i < TT / NG; ++i) {
+            // (neighbouring groups four rows apart: 8 lanes' 16-byte reads meet no bank twice)
+            const int t = NG == 4 ? og + 4 * i : (og >> 1) + 4 * (og & 1) + 8 * i;
+            const Four v = load4(vt + S::at(t, warp * CW + oc));
+#pragma unroll
+            for (int h = 0; h < GP; h += 4) {
+                const float4 p = *reinterpret_cast<const float4 *>(&sm.p[t][h]);
+                const float pp[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint64_t p2 = pack2(pp[u], pp[u]);
+                    o[h + u][0] = fma2(v.a, p2, o[h + u][0]);
+                    o[h + u][1] = fma2(v.b, p2, o[h + u][1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.empty[st]));
+            if (d.flags & kLast) mbar_arrive(smem_u32(&sm.q_empty[seg % S::QS]));
+        }
+        if (!(d.flags & kLast)) continue;
+        // ---- the end of this CTA's piece of the group: the sums of the warps, and O's parts of the NG groups of
+        // lanes, by halves of the heads
+#pragma unroll
+        for (int e = 0; e < NO; ++e) {
+            float l = l_run[e];
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if (lane < 8) sm.sum[warp][8 * e + lane] = l;
+        }
+        int h0 = 0;                        // first head of what this lane keeps
+        auto halve = [&](int bit, int keep) {
+            const bool up = lane & bit;
+#pragma unroll
+            for (int h = 0; h < GP / 2; ++h) {
+                if (h >= keep) break;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float2 f = unpack2(o[h][c]), g = unpack2(o[h + keep][c]);
+                    const float2 mine = up ? g : f, give = up ? f : g;
+                    o[h][c] = pack2(mine.x + __shfl_xor_sync(0xffffffffu, give.x, bit),
+                                    mine.y + __shfl_xor_sync(0xffffffffu, give.y, bit));
+                }
+            }
+            h0 += up ? keep : 0;
+        };
+        halve(16, GP / 2);
+        halve(8, GP / 4);
+        if (NG == 8) halve(4, GP / 8);
+        math_sync();
+        const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
+        float *part = piece_place(a, parts, d.flags);
+        auto total = [&](int h) {
+            float L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) L += sm.sum[w][h];
+            return L;
+        };
+#pragma unroll
+        for (int u = 0; u < GP / NG; ++u) {
+            const int h = h0 + u;
+            if (h >= a.G) continue;
+            const float L = part ? 1.f : total(h), inv = L == 0.f ? 0.f : 1.f / L;
+            const float2 f = unpack2(o[u][0]), g = unpack2(o[u][1]);
+            const float y[4] = {f.x * inv, f.y * inv, g.x * inv, g.y * inv};
+            store_vec<4>((part ? part + piece_ml(a.G) : static_cast<float *>(a.out) + head * D) + h * D + (warp * CW + oc) * 4, y);
+        }
+        if (warp == 0 && lane < 8) {
+#pragma unroll
+            for (int e = 0; e < NO; ++e) {
+                const int h = 8 * e + lane;
+                if (h >= a.G) continue;
+                const float L = total(h);
+                if (part) reinterpret_cast<float2 *>(part)[h] = make_float2(m_run[e], L);
+                else if (a.lse) a.lse[head + h] = L == 0.f ? -INFINITY : (m_run[e] + log2f(L)) * kLn2;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < GP; ++h) o[h][0] = o[h][1] = 0ull;
+#pragma unroll
+        for (int e = 0; e < NO; ++e) {
+            m_run[e] = -INFINITY;
+            l_run[e] = 0.f;
+        }
+        if (part) join_group<float, D>(a, parts, arrived, d, head, sm.last);
+    }
+}
+
+template <typename T, int D, int GP, bool kTma>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   float *parts, int32_t *arrived) {
-    using S = Shared<T, D>;
-    constexpr bool kBf16 = sizeof(T) == 2;
-    constexpr int TT = S::TT;
-    constexpr int ROWB = D * (int)sizeof(T), CH = ROWB / 16;       // bytes and 16-byte chunks of a row
-    constexpr int NT = TT / 32;                                     // 8-token columns of S per warp
-    constexpr int NJ = D / 32;                                      // 8-wide columns of O per warp
+    using S = Shared<T, D, GP>;
+    constexpr bool kBf16 = S::kBf16;
+    constexpr int TT = S::TT, ROWB = S::ROWB, CH = S::CH;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -480,7 +1009,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     }
                     const bool ok = r2 >= 0;
                     const int64_t at = (ok ? r2 : 0) * ROWB + ch * 16;
-                    const uint32_t to = (tok >> 3) * 8 * ROWB + (ch >> 3) * 1024 + (tok & 7) * 128 + (((ch & 7) ^ (tok & 7)) << 4);
+                    const uint32_t to = S::at(tok, ch);
                     cp16(kb + to, static_cast<const char *>(a.kpool) + at, ok);
                     cp16(vb + to, static_cast<const char *>(a.vpool) + at, ok);
                 }
@@ -501,385 +1030,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     }
 
     // ================= the computing warps
-    const int gq = lane >> 2, t4 = lane & 3;
-    // Q fragments (fp32 is split in two tf32 parts where it is used: both parts of all would not fit the registers)
-    constexpr int KS = kBf16 ? D / 16 : D / 8;
-    uint32_t qf[KS][4];
-    float o[NJ][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    const float s2 = a.s * kLog2e;
-    const int tok0 = warp * (TT / 4);
-
-    auto load_q = [&](int place) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int h = gq + 8 * half;
-            const bool ok = h < a.G;
-            if constexpr (kBf16) {
-                const uint32_t *row = reinterpret_cast<const uint32_t *>(sm.q[place][h]);
-#pragma unroll
-                for (int st = 0; st < KS; ++st) {
-                    qf[st][half] = ok ? row[st * 8 + t4] : 0u;
-                    qf[st][2 + half] = ok ? row[st * 8 + 4 + t4] : 0u;
-                }
-            } else {
-                // coordinates of 16 are dealt to the k slots so that a lane's are 4 in a row
-                const float4 *row = reinterpret_cast<const float4 *>(sm.q[place][h]);
-#pragma unroll
-                for (int st = 0; st < KS; st += 2) {
-                    const float4 x = ok ? row[st * 2 + t4] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    qf[st][half] = __float_as_uint(x.x);
-                    qf[st][2 + half] = __float_as_uint(x.y);
-                    qf[st + 1][half] = __float_as_uint(x.z);
-                    qf[st + 1][2 + half] = __float_as_uint(x.w);
-                }
-            }
-        }
-    };
-    // the token (of its 8) of column c (0, 1) of a lane's S, and the coordinate of column c of its O block j.
-    // fp32: tokens and coordinates are dealt to the MMAs' columns so that 16-byte reads meet no bank twice.
-    auto tok_of = [&](int c) { return kBf16 ? 2 * t4 + c : t4 + 4 * c; };
-    auto dim_of = [&](int j, int c) { return warp * (D / 4) + (kBf16 ? 8 * j + 2 * t4 + c : (2 * t4 + c) * NJ + j); };
-    // byte offsets of this lane's reads of K (two values of bit 2 of the chunk) and of V
-    uint32_t ko[2], vo[kBf16 ? NJ / 2 : 2];
-    {
-        const int r = kBf16 ? lane & 7 : (gq >> 1) | ((gq & 1) << 2), c = kBf16 ? lane >> 3 : t4;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) ko[b] = (tok0 >> 3) * 8 * ROWB + r * 128 + (((4 * b + c) ^ r) << 4);
-        if constexpr (kBf16) {
-#pragma unroll
-            for (int jp = 0; jp < NJ / 2; ++jp) {
-                const int ch = warp * (D / 32) + 2 * jp + (lane >> 4), rv = lane & 7;
-                vo[jp] = ((lane >> 3) & 1) * 8 * ROWB + (ch >> 3) * 1024 + rv * 128 + (((ch & 7) ^ rv) << 4);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int byte = (warp * (D / 4) + gq * NJ) * 4, ch = byte >> 4, rv = 2 * t4 + e;
-                vo[e] = (ch >> 3) * 1024 + rv * 128 + (((ch & 7) ^ rv) << 4) + (byte & 15);
-            }
-        }
-    }
-
-    // Announces this CTA's piece (or set of pieces) at a counter; true in the CTA that is the last of `of`.
-    // (The barrier puts every thread's stores before thread 0's fence, which publishes them; the pieces are
-    // read past L1.)
-    auto arrive = [&](int32_t *counter, int of) {
-        math_sync();
-        if (tid == 0) {
-            __threadfence();
-            const bool last = atomicAdd(counter, 1) == of - 1;
-            if (last) {
-                __threadfence();
-                *counter = 0;
-            }
-            sm.last = last;
-        }
-        math_sync();
-        return sm.last != 0;
-    };
-
-    int seg = -1;
-    for (int it = 0; it < n; ++it) {
-        const int st = it % kStages;
-        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
-        const Tile d = sm.tile[st];
-        if (d.flags & kFirst) {
-            ++seg;
-            load_q(seg % S::QS);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[seg % S::QS]));
-        }
-        const uint32_t kt = smem_u32(sm.ring[st]), vt = kt + kTileBytes;
-        const uint8_t *ktp = sm.ring[st], *vtp = ktp + kTileBytes;
-
-        // ---- S = Q K^T of this warp's tokens
-        float x[NT][4];
-        if constexpr (kBf16) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kp = 0; kp < D / 32; ++kp) {
-                    uint32_t b[4];
-                    ldsm4(kt + ko[kp & 1] + nt * 8 * ROWB + (kp >> 1) * 1024, b);
-                    mma_bf16(s0, qf[2 * kp], b[0], b[1]);
-                    mma_bf16(s1, qf[2 * kp + 1], b[2], b[3]);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) x[nt][u] = (s0[u] + s1[u]) * s2;
-            }
-        } else {
-            // three tf32 products (the low parts' product, 2^-22 of the whole, is left out)
-            float s0[NT][4], s1[NT][4], cr[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) s0[nt][u] = s1[nt][u] = cr[nt][u] = 0.f;
-#pragma unroll
-            for (int kp = 0; kp < D / 16; ++kp) {
-                uint32_t qh[2][4], ql[2][4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) split_tf32(__uint_as_float(qf[2 * kp + e][u]), qh[e][u], ql[e][u]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float4 kx = *reinterpret_cast<const float4 *>(ktp + ko[kp & 1] + nt * 8 * ROWB + (kp >> 1) * 1024);
-                    uint32_t h[4], w[4];
-                    split_tf32(kx.x, h[0], w[0]);
-                    split_tf32(kx.y, h[1], w[1]);
-                    split_tf32(kx.z, h[2], w[2]);
-                    split_tf32(kx.w, h[3], w[3]);
-                    mma_tf32(s0[nt], qh[0], h[0], h[1]);
-                    mma_tf32(s1[nt], qh[1], h[2], h[3]);
-                    mma_tf32(cr[nt], qh[0], w[0], w[1]);
-                    mma_tf32(cr[nt], ql[0], h[0], h[1]);
-                    mma_tf32(cr[nt], qh[1], w[2], w[3]);
-                    mma_tf32(cr[nt], ql[1], h[2], h[3]);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) x[nt][u] = with_correction(s0[nt][u] + s1[nt][u], cr[nt][u]) * s2;
-        }
-        // tokens outside the row's range or on no page
-        auto hidden = [&](int t) {
-            const int pos = d.base + t;
-            return pos < d.lo || pos >= d.hi || ((sm.tile[st].bad[t >> 5] >> (t & 31)) & 1u);
-        };
-        if (d.flags & kEdge) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (hidden(tok0 + nt * 8 + tok_of(u & 1))) x[nt][u] = -INFINITY;
-        }
-        // ---- row maxima over the tile
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mx = max_nan(mx, max_nan(x[nt][2 * r], x[nt][2 * r + 1]));
-            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            if (t4 == 0) sm.mx[warp][gq + 8 * r] = mx;
-        }
-        if (math_any(!ok)) break;          // a wait ran out: every warp leaves here
-        float corr[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float mx = m_run[r];
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = max_nan(mx, sm.mx[w][gq + 8 * r]);
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            corr[r] = ex2(m_run[r] - ref);
-            m_run[r] = mx;
-            float ls = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = ex2(x[nt][2 * r] - ref), p1 = ex2(x[nt][2 * r + 1] - ref);
-                ls += p0 + p1;
-                const int at = tok0 + nt * 8, h = gq + 8 * r;
-                if constexpr (kBf16) {
-                    const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
-                    const float2 hf = __bfloat1622float2(hi);
-                    *reinterpret_cast<__nv_bfloat162 *>(&sm.p[0][h][at + 2 * t4]) = hi;
-                    *reinterpret_cast<__nv_bfloat162 *>(&sm.p[1][h][at + 2 * t4]) = __floats2bfloat162_rn(p0 - hf.x, p1 - hf.y);
-                } else {
-                    uint32_t hi, lo;
-                    split_tf32(p0, hi, lo);
-                    sm.p[0][h][at + t4] = __uint_as_float(hi);
-                    sm.p[1][h][at + t4] = __uint_as_float(lo);
-                    split_tf32(p1, hi, lo);
-                    sm.p[0][h][at + t4 + 4] = __uint_as_float(hi);
-                    sm.p[1][h][at + t4 + 4] = __uint_as_float(lo);
-                }
-            }
-            l_run[r] = l_run[r] * corr[r] + ls;
-        }
-        math_sync();
-        // ---- the tile's P V in accumulators of its own (the MMA truncates its sums: kept short), then into O.
-        float pv[NJ][4];
-        auto weigh = [&](bool low) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) pv[j][0] = pv[j][1] = pv[j][2] = pv[j][3] = 0.f;
-            if constexpr (kBf16) {
-#pragma unroll
-                for (int kp = 0; kp < TT / 16; ++kp) {
-                    uint32_t ph[4], pl[4];
-                    const int prow = lane & 15, pcol = kp * 16 + (lane >> 4) * 8;
-                    ldsm4(smem_u32(&sm.p[0][prow][pcol]), ph);
-                    if (low) ldsm4(smem_u32(&sm.p[1][prow][pcol]), pl);
-#pragma unroll
-                    for (int jp = 0; jp < NJ / 2; ++jp) {
-                        uint32_t b[4];
-                        ldsm4t(vt + vo[jp] + kp * 16 * ROWB, b);
-                        mma_bf16(pv[2 * jp], ph, b[0], b[1]);
-                        mma_bf16(pv[2 * jp + 1], ph, b[2], b[3]);
-                        if (low) {
-                            mma_bf16(pv[2 * jp], pl, b[0], b[1]);
-                            mma_bf16(pv[2 * jp + 1], pl, b[2], b[3]);
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int kp = 0; kp < TT / 8; ++kp) {
-                    // k slots t4 and t4 + 4 are tokens 2 t4 and 2 t4 + 1
-                    uint32_t ph[4], pl[4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float2 h = *reinterpret_cast<const float2 *>(&sm.p[0][gq + 8 * u][kp * 8 + 2 * t4]);
-                        ph[u] = __float_as_uint(h.x);
-                        ph[2 + u] = __float_as_uint(h.y);
-                        if (low) {
-                            const float2 l = *reinterpret_cast<const float2 *>(&sm.p[1][gq + 8 * u][kp * 8 + 2 * t4]);
-                            pl[u] = __float_as_uint(l.x);
-                            pl[2 + u] = __float_as_uint(l.y);
-                        }
-                    }
-                    // NJ coordinates in a row per lane: column gq of each of the NJ column blocks
-                    float v0[NJ], v1[NJ];
-                    if constexpr (NJ == 4) {
-                        *reinterpret_cast<float4 *>(v0) = *reinterpret_cast<const float4 *>(vtp + vo[0] + kp * 8 * ROWB);
-                        *reinterpret_cast<float4 *>(v1) = *reinterpret_cast<const float4 *>(vtp + vo[1] + kp * 8 * ROWB);
-                    } else {
-                        *reinterpret_cast<float2 *>(v0) = *reinterpret_cast<const float2 *>(vtp + vo[0] + kp * 8 * ROWB);
-                        *reinterpret_cast<float2 *>(v1) = *reinterpret_cast<const float2 *>(vtp + vo[1] + kp * 8 * ROWB);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        uint32_t h0, h1, l0, l1;
-                        split_tf32(v0[j], h0, l0);
-                        split_tf32(v1[j], h1, l1);
-                        mma_tf32(pv[j], ph, h0, h1);
-                        if (low) {
-                            mma_tf32(pv[j], ph, l0, l1);
-                            mma_tf32(pv[j], pl, h0, h1);
-                        }
-                    }
-                }
-            }
-        };
-        weigh(true);
-        float odd = 0.f;                   // stays 0 if everything is finite
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) odd = fmaf(pv[j][u], 0.f, odd);
-        if (__any_sync(0xffffffffu, odd != 0.f)) {
-            // Hidden tokens have weight 0, but whatever their value rows hold (other sequences' rows, NaN) was
-            // multiplied by it: clear them and do the tile again. An attended infinite value times a low part
-            // can be NaN where the product is infinite: what is not finite then is taken from the high parts.
-            if (d.flags & kEdge)
-                for (int i = lane; i < TT * CH / 4; i += 32) {     // this warp's coordinates, which no other reads
-                    const int t = i / (CH / 4), ch = warp * (CH / 4) + i % (CH / 4);
-                    if (hidden(t))
-                        *reinterpret_cast<uint4 *>(sm.ring[st] + kTileBytes + (t >> 3) * 8 * ROWB + (ch >> 3) * 1024 +
-                                                   (t & 7) * 128 + (((ch & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-                }
-            __syncwarp();
-            weigh(true);
-            odd = 0.f;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) odd = fmaf(pv[j][u], 0.f, odd);
-            if (__any_sync(0xffffffffu, odd != 0.f)) {
-                float both[NJ][4];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) both[j][u] = pv[j][u];
-                weigh(false);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) pv[j][u] = fabsf(both[j][u]) <= 3.0e38f ? both[j][u] : pv[j][u];
-            }
-            fence_proxy_async_smem();      // before a later copy lands there
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) o[j][u] = fmaf(o[j][u], corr[u >> 1], pv[j][u]);
-
-        if (!(d.flags & kLast)) continue;
-        // ---- the end of this CTA's piece of the group: the sums of the warps
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float l = l_run[r];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if (t4 == 0) sm.sum[warp][gq + 8 * r] = l;
-        }
-        math_sync();
-        const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
-        float *part = nullptr;
-        if ((d.flags & (kHead | kTail)) != (kHead | kTail))        // slot 2c + 1: a group's first piece, 2c: another
-            part = parts + (2 * (int64_t)blockIdx.x + (d.flags & kHead ? 1 : 0)) * piece_floats(a.G, D);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float L = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) L += sm.sum[w][gq + 8 * r];
-            const int h = gq + 8 * r;
-            if (h < a.G) {
-                if (part) {
-                    if (warp == 0 && t4 == 0) reinterpret_cast<float2 *>(part)[h] = make_float2(m_run[r], L);
-                } else if (a.lse && warp == 0 && t4 == 0) {
-                    a.lse[head + h] = L == 0.f ? -INFINITY : (m_run[r] + log2f(L)) * kLn2;
-                }
-                const float inv = part ? 1.f : L == 0.f ? 0.f : 1.f / L;
-                // a lane's coordinates come in runs of 2 (bf16) or NJ (fp32)
-                constexpr int RUN = kBf16 ? 2 : NJ, RUNS = 2 * NJ / RUN;
-#pragma unroll
-                for (int e = 0; e < RUNS; ++e) {
-                    float y[RUN];
-#pragma unroll
-                    for (int c = 0; c < RUN; ++c) y[c] = (kBf16 ? o[e][2 * r + c] : o[c][2 * r + e]) * inv;
-                    const int at = h * D + (kBf16 ? dim_of(e, 0) : dim_of(0, e));
-                    if (part) store_vec<RUN>(part + piece_ml(a.G) + at, y);
-                    else store_vec<RUN>(static_cast<T *>(a.out) + head * D + at, y);
-                }
-            }
-            m_run[r] = -INFINITY;
-            l_run[r] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        if (!part) continue;
-
-        // ---- the last piece to arrive joins them all; with many pieces the last of a set of about sqrt(pieces)
-        // joins the set into its first piece's place, and the last set to arrive joins the sets
-        const int pieces = d.pieces, slot0 = 2 * d.c_first + 1, mine_i = (int)blockIdx.x - d.c_first;
-        int set = pieces;
-        if (pieces > kDirect) {
-            set = kDirect / 2;
-            while (set * set < pieces) ++set;
-        }
-        const int i0 = mine_i / set * set, in_set = min(set, pieces - i0), sets = (pieces + set - 1) / set;
-        const int set0 = i0 == 0 ? slot0 : 2 * (d.c_first + i0);
-        int32_t *counter = arrived + set0;
-        int cnt = in_set, s0 = set0, s1 = 2 * (d.c_first + i0 + 1), step = 2;
-        bool back = sets > 1;
-#pragma unroll 1
-        while (arrive(counter, cnt)) {
-            join<T, D>(a, parts, cnt, s0, s1, step, head, back);
-            if (!back) break;
-            counter = arrived + 2 * kMaxWorkers + slot0;       // now the sets
-            cnt = sets;
-            s0 = slot0;
-            s1 = 2 * (d.c_first + set);
-            step = 2 * set;
-            back = false;
-        }
-    }
+    if constexpr (kBf16) math_bf16<D>(a, sm, parts, arrived, n);
+    else math_f32<D, GP>(a, sm, parts, arrived, n);
     // ---- rows that attend nothing
     for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const RowSpan s = row_span(a, r);
@@ -907,15 +1059,15 @@ bool pool_map(CUtensorMap *map, const void *pool, const PagedAttnArgs &a, int bo
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool kTma>
+template <typename T, int D, int GP, bool kTma>
 cudaError_t launch(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaStream_t st) {
-    const size_t smem = sizeof(Shared<T, D>);
-    static_assert(2 * (sizeof(Shared<T, D>) + 1024) <= 228 * 1024, "two CTAs per SM");
+    const size_t smem = sizeof(Shared<T, D, GP>);
+    static_assert(2 * (sizeof(Shared<T, D, GP>) + 1024) <= 228 * 1024, "two CTAs per SM");
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, GP, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
@@ -927,16 +1079,22 @@ cudaError_t launch(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaS
     }
     // no more CTAs than the longest possible rows would keep busy
     const int64_t longest = min64((int64_t)a.max_pages << a.lps, a.window > 0 ? (int64_t)a.window + kBox : INT64_MAX);
-    const int64_t tiles = (longest + Shared<T, D>::TT - 1) / Shared<T, D>::TT * a.Hkv * a.rows;
+    const int64_t tiles = (longest + Shared<T, D, GP>::TT - 1) / Shared<T, D, GP>::TT * a.Hkv * a.rows;
     const int grid = (int)max64(1, min64(kMaxWorkers, (tiles + kMinTiles - 1) / kMinTiles));
     ProfScope ps("paged_decode", st);
-    return launch_pdl(paged_attn_kernel<T, D, kTma>, dim3(grid), dim3(kThreads), smem, st, a, kmap, vmap, parts, arrived);
+    return launch_pdl(paged_attn_kernel<T, D, GP, kTma>, dim3(grid), dim3(kThreads), smem, st, a, kmap, vmap, parts, arrived);
 }
 
 // Pages of 8 rows and more are copied by TMA, whose boxes are whole blocks of 8 rows; smaller ones row by row.
-template <typename T, int D>
+template <typename T, int D, int GP>
 cudaError_t launch_page(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaStream_t st) {
-    return a.lps >= 3 ? launch<T, D, true>(a, parts, arrived, st) : launch<T, D, false>(a, parts, arrived, st);
+    return a.lps >= 3 ? launch<T, D, GP, true>(a, parts, arrived, st) : launch<T, D, GP, false>(a, parts, arrived, st);
+}
+
+template <int D>
+cudaError_t launch_dim(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaStream_t st) {
+    if (a.dtype == ZHA_BF16) return launch_page<__nv_bfloat16, D, kRows>(a, parts, arrived, st);
+    return a.G <= 8 ? launch_page<float, D, 8>(a, parts, arrived, st) : launch_page<float, D, 16>(a, parts, arrived, st);
 }
 
 size_t pieces_bytes(const PagedAttnArgs &a) { return (size_t)kMaxWorkers * 2 * piece_floats(a.G, a.d) * sizeof(float); }
@@ -949,10 +1107,7 @@ size_t paged_attn_workspace(const PagedAttnArgs &a) { return pieces_bytes(a) + 4
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, cudaStream_t st) {
     float *parts = static_cast<float *>(a.ws);
     int32_t *arrived = reinterpret_cast<int32_t *>(static_cast<char *>(a.ws) + pieces_bytes(a));
-    if (a.dtype == ZHA_BF16)
-        return a.d == 128 ? launch_page<__nv_bfloat16, 128>(a, parts, arrived, st)
-                          : launch_page<__nv_bfloat16, 64>(a, parts, arrived, st);
-    return a.d == 128 ? launch_page<float, 128>(a, parts, arrived, st) : launch_page<float, 64>(a, parts, arrived, st);
+    return a.d == 128 ? launch_dim<128>(a, parts, arrived, st) : launch_dim<64>(a, parts, arrived, st);
 }
 
 }  // namespace zha
