@@ -492,7 +492,8 @@ ZHA_API zha_status zha_rotary_freqs(int32_t rotary_dim, double base, int32_t sca
  * k may be absent (null, with its output). transpose != 0 applies the
  * transposed map, which is the gradient of the rotation (and, for mscale 1,
  * its inverse). Sines and cosines come from fp64 angles, products are fp32,
- * each output is rounded once. dtype ZHA_BF16 or ZHA_F32, head_dim 64 or 128.
+ * each output is rounded once. dtype ZHA_BF16 or ZHA_F32, head_dim 64 or 128,
+ * at most 1,024 heads each and 2^30 tokens, strides below 2^30 elements.
  */
 ZHA_API zha_status zha_rotary_apply(const zha_rotary *rotary, int32_t head_dim, int32_t dtype,
                                     int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
@@ -510,7 +511,8 @@ ZHA_API zha_status zha_rotary_apply(const zha_rotary *rotary, int32_t head_dim, 
  * then), q may be null (with q_out). q_out is contiguous and may be q where q
  * is contiguous; q_stride, k_stride, v_stride as in zha_rotary_apply. Slots
  * of different tokens are distinct; where two are equal the cache row's
- * contents are unspecified (some of each).
+ * contents are unspecified (some of each). At most 1,024 heads and 2^30
+ * tokens.
  */
 ZHA_API zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary *rotary,
                                    int32_t n_tokens, const void *q, int64_t q_stride, const void *k_new,

@@ -444,6 +444,48 @@ def test_decode_on_other_streams(zha):
     assert torch.equal(outs[0], want[0][0]) and torch.equal(outs[1], want[1][0])
 
 
+def test_decode_many_rows_and_one_workspace(zha):
+    """More rows than a warp or a CTA has threads, empty and left-out ones among them; one workspace for calls of
+    different row counts, one after the other."""
+    rng = random.Random(17)
+    lens = [rng.choice([0, 1, 40, 200, 700]) for _ in range(50)]
+    c = Case(zha, lens, 8, 4, 64, 16, BF16, seed=18)
+    n = 700
+    seq = [rng.randint(-1, 49) for _ in range(n)]
+    ws = zha.paged_workspace(c.cfg, n)
+    q = c.queries(n)
+    out, lse = c.run(q, ws, seq_ids=ints(seq))
+    c.check(q, out, lse, [(r, seq[r], lens[seq[r]]) for r in range(0, n, 7) if seq[r] >= 0])
+    for r in range(n):
+        if seq[r] < 0:
+            assert torch.all(out[r] == 77)
+    few = c.run(q[:20].contiguous(), ws, seq_ids=ints(seq[:20]))
+    c.check(q, few[0], few[1], [(r, seq[r], lens[seq[r]]) for r in range(20) if seq[r] >= 0])
+    again = c.run(q, ws, seq_ids=ints(seq))
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_empty_calls_and_queries_in_place(zha, dt):
+    cfg = zha.paged_config(2, 4, 2, 64, 16, 6, 3, dtype=NAME[dt])
+    kp, vp = (torch.zeros(6, 2, 16, 64, dtype=dt, device="cuda") for _ in range(2))
+    rot = zha.Rotary(64)
+    none = ints([])
+    q0, k0 = torch.zeros(0, 4, 64, dtype=dt, device="cuda"), torch.zeros(0, 2, 64, dtype=dt, device="cuda")
+    zha.rotary(rot, q0, k0, none)
+    zha.paged_write(cfg, rot, q0, k0, k0, none, none, q0, kp, vp)
+    zha.paged_decode(cfg, q0, kp, vp, ints([0] * 6), ints([0, 0]), q0, zha.paged_workspace(cfg, 1))
+    g = torch.Generator().manual_seed(20)
+    q, k = (torch.randn(9, h, 64, generator=g).to(dt).cuda() for h in (4, 2))
+    pos, slots = ints(list(range(50, 59))), ints([3, -1, 5, 90, 7, 8, 9, -1, 11])
+    want = torch.empty_like(q)
+    zha.rotary(rot, q, None, pos, want)
+    want[1], want[7] = q[1], q[7]                                     # skipped rows stay
+    zha.paged_write(cfg, rot, q, k, k, pos, slots, q, kp, vp)         # q_out is q
+    assert torch.equal(q, want)
+    torch.cuda.synchronize()
+
+
 # ---------------------------------------------------------------- steps
 
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])

@@ -9,7 +9,12 @@ namespace {
 
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-zha_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ZHA_OK : ZHA_ERR_CUDA; }
+// The launch's error is the call's; it is not left for the host program's next look at the last error.
+zha_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return ZHA_OK;
+    (void)cudaGetLastError();
+    return ZHA_ERR_CUDA;
+}
 
 int log2i(int x) {
     int l = 0;
@@ -46,7 +51,7 @@ zha_status check_rotary(const zha_rotary *r, int head_dim) {
 bool stride_ok(int64_t *stride, int heads, int d, int es) {
     const int64_t row = (int64_t)heads * d;
     if (*stride == 0) *stride = row;
-    return *stride >= row && (*stride * es) % 16 == 0 && *stride < (int64_t(1) << 40);
+    return *stride >= row && (*stride * es) % 16 == 0 && *stride < (int64_t(1) << 30);
 }
 
 zha::PagedAttnArgs attn_args(const zha_paged_config *c, int rows) {
@@ -139,11 +144,13 @@ zha_status zha_rotary_apply(const zha_rotary *rotary, int32_t head_dim, int32_t 
     if (dtype != ZHA_BF16 && dtype != ZHA_F32) return ZHA_ERR_UNSUPPORTED;
     zha_status s = check_rotary(rotary, head_dim);
     if (s != ZHA_OK) return s;
-    if (n_tokens < 0 || (!q && !k) || !q != !q_out || !k != !k_out) return ZHA_ERR_INVALID_ARG;
+    if (n_tokens < 0) return ZHA_ERR_INVALID_ARG;
+    if (n_tokens == 0) return ZHA_OK;
+    if (n_tokens > (1 << 30)) return ZHA_ERR_UNSUPPORTED;
+    if ((!q && !k) || !q != !q_out || !k != !k_out) return ZHA_ERR_INVALID_ARG;
     if ((q && n_q_heads < 1) || (k && n_k_heads < 1)) return ZHA_ERR_INVALID_ARG;
     const int Hq = q ? n_q_heads : 0, Hk = k ? n_k_heads : 0;
     if (Hq > 1024 || Hk > 1024) return ZHA_ERR_UNSUPPORTED;
-    if (n_tokens == 0) return ZHA_OK;
     if (!positions || !aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
         return ZHA_ERR_INVALID_ARG;
     const int es = dtype == ZHA_BF16 ? 2 : 4;
@@ -182,9 +189,10 @@ zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary *rotary
     zha_status s = check_paged(cfg);
     if (s != ZHA_OK) return s;
     if (rotary && (s = check_rotary(rotary, cfg->head_dim)) != ZHA_OK) return s;
-    if (n_tokens < 0 || !q != !q_out) return ZHA_ERR_INVALID_ARG;
-    if (cfg->n_q_heads > 1024 || cfg->n_kv_heads > 1024) return ZHA_ERR_UNSUPPORTED;
+    if (n_tokens < 0) return ZHA_ERR_INVALID_ARG;
     if (n_tokens == 0) return ZHA_OK;
+    if (n_tokens > (1 << 30) || cfg->n_q_heads > 1024 || cfg->n_kv_heads > 1024) return ZHA_ERR_UNSUPPORTED;
+    if (!q != !q_out) return ZHA_ERR_INVALID_ARG;
     if (!k_new || !v_new || !slots || !kpool || !vpool || (rotary && !positions)) return ZHA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(kpool) ||
         !aligned16(vpool))

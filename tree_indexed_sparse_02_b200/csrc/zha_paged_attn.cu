@@ -41,7 +41,7 @@ constexpr int kStages = 3;
 constexpr int kRows = 16;                // query heads of a group, padded to the MMA's rows
 constexpr int kTileBytes = 16384;        // of K, and of V
 constexpr int kMaxWorkers = 148 * 2;
-constexpr int kMinTiles = 4;             // tiles of a CTA's part at least
+constexpr int kMinTiles = 3;             // tiles of a CTA's part at least
 constexpr int kBox = 16;                 // rows of a page copied at a time, at most
 constexpr int kDirect = 16;              // pieces of a group joined at once; more in two levels
 constexpr int kSnap = 2;                 // a CTA's part begins at a group's border if one is this near (in tiles)
@@ -163,7 +163,7 @@ struct Shared {
     int edge_row[2], edge_before[2], edge_tiles[2];
     int scan[kThreads / 32];
     uint64_t full[kStages], empty[kStages], q_empty[QS];
-    int last, abort;
+    int n, last, abort;
 
     // byte offset of a token's 16-byte chunk in K or V of a tile
     static __device__ __forceinline__ int at(int t, int ch) {
@@ -803,76 +803,81 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     pdl_wait();
 
     // ---- this CTA's part [w0, w1) of the list of all tiles, and the row it begins in: prefix sums over the
-    // rows, by every warp for itself where a warp holds them all
+    // rows, by the copying warp alone where it holds them all. (The others get its count, so that they cannot
+    // disagree on it.)
     auto tiles_of = [&](const RowSpan &s) { return s.hi > s.lo ? (s.hi - (s.lo & -box) + TT - 1) / TT : 0; };
     const bool few = a.rows <= 32;
-    const int per = few ? 1 : (a.rows + kThreads - 1) / kThreads;
-    const int ra = min((few ? lane : tid) * per, a.rows), rb = min(ra + per, a.rows);
-    int mine = 0;
-    for (int r = ra; r < rb; ++r) mine += tiles_of(row_span(a, r));
-    int before = mine;                   // first inclusive, of this warp's lanes
+    int w0 = 0, w1 = 0, share = 1, start_row = 0, start_before = 0;
+    if (!few || warp == kWarps) {
+        const int per = few ? 1 : (a.rows + kThreads - 1) / kThreads;
+        const int ra = min((few ? lane : tid) * per, a.rows), rb = min(ra + per, a.rows);
+        int mine = 0;
+        for (int r = ra; r < rb; ++r) mine += tiles_of(row_span(a, r));
+        int before = mine;               // first inclusive, of this warp's lanes
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += y;
-    }
-    int W = __shfl_sync(0xffffffffu, before, 31);
-    before -= mine;
-    if (!few) {
-        if (lane == 0) sm.scan[warp] = W;
-        __syncthreads();
-        W = 0;
-#pragma unroll 1
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sm.scan[w];
-            W += sm.scan[w];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
         }
-    }
-    W *= a.Hkv;
-    // Parts of `share` tiles, their ends moved to a group's border where one is within kSnap tiles: a piece of a
-    // few tiles costs more to join than to compute.
-    const int share = max(kMinTiles, (W + (int)gridDim.x - 1) / (int)gridDim.x);
-    int w0 = 0, w1 = 0, start_row = 0, start_before = 0;
-    const int first_tile = min((int64_t)blockIdx.x * share, (int64_t)W);
-#pragma unroll 1
-    for (int e = 0; e < 2; ++e) {        // (a loop, not two copies: the code is cold)
-        int edge = e ? min(first_tile + share, W) : first_tile;
-        const bool own = edge >= before * a.Hkv && edge < (before + mine) * a.Hkv;
-        int row = ra, t = mine, at = before;
-        if (few) {
-            const int src = (__ffs(__ballot_sync(0xffffffffu, own)) - 1) & 31;
-            row = __shfl_sync(0xffffffffu, ra, src);
-            t = __shfl_sync(0xffffffffu, mine, src);
-            at = __shfl_sync(0xffffffffu, before, src);
-        } else {
-            if (own) {
-                for (row = ra; row < rb; ++row) {
-                    t = tiles_of(row_span(a, row));
-                    if (edge < (at + t) * a.Hkv) break;
-                    at += t;
-                }
-                sm.edge_row[e] = row;
-                sm.edge_tiles[e] = t;
-                sm.edge_before[e] = at;
-            }
+        int W = __shfl_sync(0xffffffffu, before, 31);
+        before -= mine;
+        if (!few) {
+            if (lane == 0) sm.scan[warp] = W;
             __syncthreads();
-            row = sm.edge_row[e];
-            t = sm.edge_tiles[e];
-            at = sm.edge_before[e];
+            W = 0;
+#pragma unroll 1
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) before += sm.scan[w];
+                W += sm.scan[w];
+            }
         }
-        if (e == 0) {
-            start_row = row;
-            start_before = at;
+        W *= a.Hkv;
+        // Parts of `share` tiles, their ends moved to a group's border where one is within kSnap tiles: a piece of
+        // a few tiles costs more to join than to compute.
+        share = max(kMinTiles, (W + (int)gridDim.x - 1) / (int)gridDim.x);
+        const int first_tile = min((int64_t)blockIdx.x * share, (int64_t)W);
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {    // (a loop, not two copies: the code is cold)
+            int edge = e ? min(first_tile + share, W) : first_tile;
+            const bool own = edge >= before * a.Hkv && edge < (before + mine) * a.Hkv;
+            int row = ra, t = mine, at = before;
+            if (few) {
+                const int src = (__ffs(__ballot_sync(0xffffffffu, own)) - 1) & 31;
+                row = __shfl_sync(0xffffffffu, ra, src);
+                t = __shfl_sync(0xffffffffu, mine, src);
+                at = __shfl_sync(0xffffffffu, before, src);
+            } else {
+                if (own) {
+                    for (row = ra; row < rb; ++row) {
+                        t = tiles_of(row_span(a, row));
+                        if (edge < (at + t) * a.Hkv) break;
+                        at += t;
+                    }
+                    sm.edge_row[e] = min(row, a.rows - 1);
+                    sm.edge_tiles[e] = t;
+                    sm.edge_before[e] = at;
+                }
+                __syncthreads();
+                row = sm.edge_row[e];
+                t = sm.edge_tiles[e];
+                at = sm.edge_before[e];
+            }
+            if (e == 0) {
+                start_row = row;
+                start_before = at;
+            }
+            if (edge > 0 && edge < W) {
+                const int i = (edge - at * a.Hkv) % t;
+                if (t - i <= kSnap) edge += t - i;
+                else if (i <= kSnap) edge -= i;
+            }
+            if (e == 0) w0 = edge;
+            else w1 = edge;
         }
-        if (edge > 0 && edge < W) {
-            const int i = (edge - at * a.Hkv) % t;
-            if (t - i <= kSnap) edge += t - i;
-            else if (i <= kSnap) edge -= i;
-        }
-        if (e == 0) w0 = edge;
-        else w1 = edge;
     }
-    const int n = w1 - w0;
+    if (tid == kMath) sm.n = w1 - w0;
+    __syncthreads();
+    const int n = sm.n;
 
     if (warp == kWarps) {
         // ================= the copying warp
@@ -895,7 +900,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             do {
                 next.span = row_span(a, ++next.r);
                 next.len = tiles_of(next.span);
-            } while (next.len == 0);
+            } while (next.len == 0 && next.r + 1 < a.rows);
         };
         if (next.kvh == a.Hkv) next_row();         // the start moved up to the end of its row
         // A lane looks up one box's page of one of the next `batch` tiles of a group (TMA), or the pages of
