@@ -129,7 +129,7 @@ __host__ __device__ __forceinline__ int piece_ml(int G) { return (2 * G + 3) & ~
 __host__ __device__ __forceinline__ int piece_floats(int G, int d) { return piece_ml(G) + G * d; }
 
 // One tile of a group, as the copying warp describes it to the others.
-struct Tile {
+struct alignas(16) Tile {
     int r, kvh;
     int flags;
     int base, lo, hi; // first token, and the tokens the row attends
@@ -909,7 +909,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         const int lbox = 31 - __clz(box), boxes = kTma ? TT >> lbox : 1, lboxes = 31 - __clz(boxes);
         const int batch = kTma ? 32 >> lboxes : 1;
         const int lt = kTma ? lane >> lboxes : 0, lb = kTma ? lane & (boxes - 1) : 0;
-        int page[NP], page_next[NP];
+        int page_next[NP];
         auto token = [&](const Walk &c, int i) {
             return (c.span.lo & -box) + (c.i + lt) * TT + (kTma ? lb * box : lane + 32 * i);
         };
@@ -923,15 +923,39 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         };
         look();
         int k = 0, seg = -1;               // tiles issued, pieces begun
-        Walk c = next;
+        int st = 0, round = 0;             // place in the ring, times round it
         int left = 0, off = 0;             // tiles left of the batch, and the next one's place in it
-        for (; k < n; ++k, --left, ++off) {
+        int64_t row[NP];                   // first row of this lane's copy in its pool, -1: none
+        uint32_t good[NP], bad[NP];        // lanes whose copy is one; whose page number is no page
+        Tile d;
+        int ci = 0, last_ci = 0;           // the next tile's place in its group, and the piece's last one
+        for (; k < n; ++k, --left, ++off, ++ci) {
             if (left == 0) {
-                c = next;
+                // what the tiles of a batch have in common
+                const Walk c = next;
                 off = 0;
+                ci = c.i;
+                last_ci = c.len - 1;
                 left = min(batch, c.len - c.i);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) page[i] = page_next[i];
+                for (int i = 0; i < NP; ++i) {
+                    const int pos = token(c, i);
+                    const bool in = lt < left && pos < c.span.hi, ok = in && (unsigned)page_next[i] < (unsigned)a.n_pages;
+                    row[i] = ok ? (((int64_t)page_next[i] * a.Hkv + c.kvh) << a.lps) + (pos & ((1 << a.lps) - 1)) : -1;
+                    good[i] = __ballot_sync(0xffffffffu, ok);
+                    bad[i] = __ballot_sync(0xffffffffu, in && !ok);
+                    if (in && !ok) set_status(a.status, ZHA_ERR_INVALID_ARG);
+                }
+                d.r = c.r;
+                d.kvh = c.kvh;
+                d.lo = c.span.lo;
+                d.hi = c.span.hi;
+                d.base = (c.span.lo & -box) + ci * TT;
+                d.flags = (c.g0 >= w0 ? kHead : 0) | (c.g0 + c.len <= w1 ? kTail : 0);
+                // of a split group: the parts that begin inside it, not near its borders
+                const int lo = (c.g0 + kSnap) / share + 1, hi = (c.g0 + c.len - kSnap - 1) / share;
+                d.c_first = lo - 1;
+                d.pieces = hi - lo + 2;
                 if (k + left < n) {
                     next.i += left;
                     if (next.i == next.len) {
@@ -942,58 +966,40 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     look();
                 }
             }
-            const int st = k % kStages, ci = c.i + off;
-            Tile d;
-            d.r = c.r;
-            d.kvh = c.kvh;
-            d.base = (c.span.lo & -box) + ci * TT;
-            d.lo = c.span.lo;
-            d.hi = c.span.hi;
-            d.flags = ((k == 0 || ci == 0) ? kFirst : 0) | ((k == n - 1 || ci == c.len - 1) ? kLast : 0) |
-                      (c.g0 >= w0 ? kHead : 0) | (c.g0 + c.len <= w1 ? kTail : 0) |
-                      ((d.base < d.lo || d.base + TT > d.hi) ? kEdge : 0);
-            if ((d.flags & kLast) && (d.flags & (kHead | kTail)) != (kHead | kTail)) {
-                // the parts that begin inside the group, not near its borders
-                const int lo = (c.g0 + kSnap) / share + 1, hi = (c.g0 + c.len - kSnap - 1) / share;
-                d.c_first = lo - 1;
-                d.pieces = hi - lo + 2;
-            }
-            d.bad[0] = d.bad[1] = d.bad[2] = d.bad[3] = 0;
-            int64_t row[NP];               // first row of the copy in its pool, -1: none
+            const bool first = k == 0 || ci == 0;
+            Tile t = d;
+            t.flags |= (first ? kFirst : 0) | (k == n - 1 || ci == last_ci ? kLast : 0) |
+                       (d.base < d.lo || d.base + TT > d.hi ? kEdge : 0);
+            d.base += TT;
+            t.bad[0] = t.bad[1] = t.bad[2] = t.bad[3] = 0;
+            const uint32_t mine = kTma ? ((1u << boxes) - 1u) << (off << lboxes) : 0xffffffffu;   // the tile's lanes
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int pos = token(c, i);
-                const bool in = (!kTma || lt == off) && pos < c.span.hi, ok = in && (unsigned)page[i] < (unsigned)a.n_pages;
-                row[i] = ok ? (((int64_t)page[i] * a.Hkv + c.kvh) << a.lps) + (pos & ((1 << a.lps) - 1)) : -1;
-                uint32_t bad = __ballot_sync(0xffffffffu, in && !ok);
-                if (bad) {
-                    if (in && !ok) set_status(a.status, ZHA_ERR_INVALID_ARG);
-                    d.flags |= kEdge;
+            for (int i = 0; i < NP; ++i)
+                if (bad[i] & mine) {
+                    t.flags |= kEdge;
                     if constexpr (kTma) {
-                        bad >>= off << lboxes;     // one bit a box
+                        const uint32_t b = (bad[0] & mine) >> (off << lboxes);     // one bit a box
 #pragma unroll
                         for (int w = 0; w < (TT + 31) / 32; ++w)
-                            for (int t = 0; t < 32; ++t)
-                                if ((bad >> ((32 * w + t) >> lbox)) & 1u) d.bad[w] |= 1u << t;
+                            for (int e = 0; e < 32; ++e)
+                                if ((b >> ((32 * w + e) >> lbox)) & 1u) t.bad[w] |= 1u << e;
                     } else {
-                        d.bad[i] = bad;
+                        t.bad[i] = bad[i];
                     }
                 }
-            }
-            if (k >= kStages && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.empty[st]), (k / kStages - 1) & 1,
-                                                                           kWaitCycles, abort, a.status)))
+            if (round > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.empty[st]), (round - 1) & 1, kWaitCycles,
+                                                                        abort, a.status)))
                 break;
-            const bool first = d.flags & kFirst;
             seg += first;
             // a piece's queries come with its first tile, once the warps hold those that were in their place
             if (first && seg >= S::QS && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.q_empty[seg % S::QS]),
                                                                                     (seg / S::QS - 1) & 1, kWaitCycles, abort, a.status)))
                 break;
             const uint32_t kb = smem_u32(sm.ring[st]), vb = kb + kTileBytes, full = smem_u32(&sm.full[st]);
-            if (lane == 0) sm.tile[st] = d;
+            if (lane == 0) sm.tile[st] = t;
             if constexpr (kTma) {
-                const bool ok = row[0] >= 0;
-                const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
+                const bool ok = row[0] >= 0 && lt == off;
+                const uint32_t cnt = __popc(good[0] & mine);
                 if (lane == 0) mbar_expect_tx(full, cnt * 2u * (uint32_t)box * ROWB + (first ? a.G * ROWB : 0));
                 __syncwarp();
                 if (ok) {
@@ -1024,8 +1030,12 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 __syncwarp();
             }
             if (first && lane < a.G)
-                bulk_load(smem_u32(sm.q[seg % S::QS][lane]), static_cast<const T *>(a.q) + ((int64_t)d.r * a.Hq + d.kvh * a.G + lane) * D,
+                bulk_load(smem_u32(sm.q[seg % S::QS][lane]), static_cast<const T *>(a.q) + ((int64_t)t.r * a.Hq + t.kvh * a.G + lane) * D,
                           ROWB, full);
+            if (++st == kStages) {
+                st = 0;
+                ++round;
+            }
         }
         // given up: the copies in flight still land before the CTA may end
         if (k < n)
