@@ -153,6 +153,7 @@ struct Shared {
     // half an ulp of the output), padded against bank conflicts; fp32: [token][head].
     typedef typename std::conditional<kBf16, __nv_bfloat16[2][kRows][TT + 8], float[TT][kRows]>::type Weights;
     alignas(16) Weights p;
+    alignas(16) float score[!kBf16 && D == 128 && GP == 16 ? TT : 1][kRows];     // between a tile's scores and its weights
     // the queries of a piece, in one of QS places; bf16 rows are padded (read as fragments: no bank twice)
     static constexpr int QROW = ROWB + (kBf16 ? 16 : 0), QS = kBf16 || GP == 8 ? 2 : 1;
     alignas(16) uint8_t q[QS][kBf16 ? kRows : GP][QROW];
@@ -574,17 +575,22 @@ __device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D
         if (d.flags & kFirst) ++seg;
         const uint8_t *kt = sm.ring[st], *vt = kt + kTileBytes, *qp = sm.q[seg % S::QS][0];
 
-        // ---- S
-        float x[NO][NX];
+        // ---- S, an octet of heads at a time. 16 heads of 128 coordinates: loops stay rolled and the scores go to
+        // shared memory (unrolled, with the scores in registers, they spill: 160 instead of 116 us at 6 x 20,001
+        // tokens); otherwise unrolling is faster by a tenth.
+        constexpr bool kRoll = D == 128 && GP == 16;
+        float kept[kRoll ? 1 : NO][kRoll ? 1 : NX];
+        const bool edge = d.flags & kEdge;
+#pragma unroll(kRoll ? 1 : NO)
+        for (int e = 0; e < NO; ++e) {
+            float mx = -INFINITY;
+#pragma unroll(kRoll ? 1 : NC)
+            for (int c = 0; c < NC; ++c) {
+                Four k[TC][CL];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            Four k[TC][CL];
+                for (int i = 0; i < TC; ++i)
 #pragma unroll
-            for (int i = 0; i < TC; ++i)
-#pragma unroll
-                for (int j = 0; j < CL; ++j) k[i][j] = load4(kt + S::at(tok0 + ts + 2 * (c * TC + i), dq + 16 * j));
-#pragma unroll
-            for (int e = 0; e < NO; ++e) {
+                    for (int j = 0; j < CL; ++j) k[i][j] = load4(kt + S::at(tok0 + ts + 2 * (c * TC + i), dq + 16 * j));
                 float v[TC][8];
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
@@ -606,51 +612,41 @@ __device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D
                     }
                 }
                 // sums over the 16 lanes: by halves of the tokens, then of the heads
-                float w[TC / 2][8], u[TC / 2][4], y[TC / 2][2];
 #pragma unroll
                 for (int i = 0; i < TC / 2; ++i) {
+                    float w[8], u[4], y[2];
 #pragma unroll
                     for (int h = 0; h < 8; ++h) {
                         const float keep = th ? v[i + TC / 2][h] : v[i][h], give = th ? v[i][h] : v[i + TC / 2][h];
-                        w[i][h] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+                        w[h] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
                     }
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const bool up = lane & 4;
-                        const float keep = up ? w[i][h + 4] : w[i][h], give = up ? w[i][h] : w[i][h + 4];
-                        u[i][h] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+                        const float keep = up ? w[h + 4] : w[h], give = up ? w[h] : w[h + 4];
+                        u[h] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const bool up = lane & 2;
-                        const float keep = up ? u[i][h + 2] : u[i][h], give = up ? u[i][h] : u[i][h + 2];
-                        y[i][h] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                        const float keep = up ? u[h + 2] : u[h], give = up ? u[h] : u[h + 2];
+                        y[h] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
                     }
                     const bool up = lane & 1;
-                    const float keep = up ? y[i][1] : y[i][0], give = up ? y[i][0] : y[i][1];
-                    x[e][c * (TC / 2) + i] = (keep + __shfl_xor_sync(0xffffffffu, give, 1)) * s2;
+                    const float keep = up ? y[1] : y[0], give = up ? y[0] : y[1];
+                    float x = (keep + __shfl_xor_sync(0xffffffffu, give, 1)) * s2;
+                    const int t = tok_of(c * (TC / 2) + i);
+                    if (edge && sm.hidden(d, st, t)) x = -INFINITY;
+                    if constexpr (kRoll) sm.score[t][8 * e + hd] = x;
+                    else kept[e][c * (TC / 2) + i] = x;
+                    mx = max_nan(mx, x);
                 }
             }
-        }
-        if (d.flags & kEdge) {
-#pragma unroll
-            for (int i = 0; i < NX; ++i)
-                if (sm.hidden(d, st, tok_of(i))) {
-#pragma unroll
-                    for (int e = 0; e < NO; ++e) x[e][i] = -INFINITY;
-                }
-            sm.clear_hidden(d, st, warp, lane);
-        }
-        // ---- maxima over the tile
-#pragma unroll
-        for (int e = 0; e < NO; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NX; ++i) mx = max_nan(mx, x[e][i]);
             mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             if (lane < 8) sm.mx[warp][8 * e + lane] = mx;
         }
+        if (edge) sm.clear_hidden(d, st, warp, lane);
         if (math_any(!ok)) break;          // a wait ran out: every warp leaves here
 #pragma unroll
         for (int e = 0; e < NO; ++e) {
@@ -663,9 +659,13 @@ __device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D
             float ls = 0.f;
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
-                const float p = ex2(x[e][i] - ref);
+                const int t = tok_of(i);
+                float x;
+                if constexpr (kRoll) x = sm.score[t][h];
+                else x = kept[e][i];
+                const float p = ex2(x - ref);
                 ls += p;
-                sm.p[tok_of(i)][h] = p;
+                sm.p[t][h] = p;
             }
             l_run[e] = l_run[e] * corr + ls;
             if (tid < 8) sm.corr[h] = corr;
@@ -716,24 +716,21 @@ __device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D
             if (lane < 8) sm.sum[warp][8 * e + lane] = l;
         }
         int h0 = 0;                        // first head of what this lane keeps
-        auto halve = [&](int bit, int keep) {
-            const bool up = lane & bit;
+        auto halve = [&]<int BIT, int KEEP>() {
+            const bool up = lane & BIT;
 #pragma unroll
-            for (int h = 0; h < GP / 2; ++h) {
-                if (h >= keep) break;
+            for (int h = 0; h < KEEP; ++h)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float2 f = unpack2(o[h][c]), g = unpack2(o[h + keep][c]);
-                    const float2 mine = up ? g : f, give = up ? f : g;
-                    o[h][c] = pack2(mine.x + __shfl_xor_sync(0xffffffffu, give.x, bit),
-                                    mine.y + __shfl_xor_sync(0xffffffffu, give.y, bit));
+                    const uint64_t mine = up ? o[h + KEEP][c] : o[h][c], give = up ? o[h][c] : o[h + KEEP][c];
+                    const float2 f = unpack2(mine), g = unpack2(give);
+                    o[h][c] = pack2(f.x + __shfl_xor_sync(0xffffffffu, g.x, BIT), f.y + __shfl_xor_sync(0xffffffffu, g.y, BIT));
                 }
-            }
-            h0 += up ? keep : 0;
+            h0 += up ? KEEP : 0;
         };
-        halve(16, GP / 2);
-        halve(8, GP / 4);
-        if (NG == 8) halve(4, GP / 8);
+        halve.template operator()<16, GP / 2>();
+        halve.template operator()<8, GP / 4>();
+        if constexpr (NG == 8) halve.template operator()<4, GP / 8>();
         math_sync();
         const int64_t head = (int64_t)d.r * a.Hq + d.kvh * a.G;
         float *part = piece_place(a, parts, d.flags);

@@ -60,7 +60,7 @@ __device__ __forceinline__ float2 cos_sin(int n, double f, float m, float sign) 
 enum { kHalf = 0, kInterleaved = 1, kStaged = 2 };
 
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const __grid_constant__ RotaryArgs a, int share) {
+__global__ void __launch_bounds__(kWarps * 32, 4) rotary_kernel(const __grid_constant__ RotaryArgs a, int share) {
     constexpr int V = Vec<T>::N, NP = D / (2 * V), HW = 32 / NP;   // HW: heads of a warp at a time
     constexpr int PL = D / 64;                                      // pairs whose sine a lane forms
     __shared__ Vec<T> staged[MODE == kStaged ? kWarps : 1][MODE == kStaged ? 64 : 1];
