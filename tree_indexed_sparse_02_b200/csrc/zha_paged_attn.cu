@@ -8,23 +8,32 @@
 // split of the tokens gives the same result.
 //
 // Bound: one read of the attended K and V rows from HBM (8 flops a byte at 8
-// query heads per KV head, far below the tensor cores' rate).
+// query heads per KV head, far below the tensor cores' rate). B200, launches in
+// a graph: 4 rows of 262,144 tokens, 32/4 heads, d 128, bf16 332 us (2.15 GB:
+// 6.47 TB/s, 99% of the measured copy); 64 rows of 16 to 16,384 tokens 79 us
+// (83%); one row of 200 tokens 7.9 us (latency: code and translations are cold
+// in every launch); fp32, 6 rows of 60,001 tokens, 16/2 heads, d 64, 82 us (69%,
+// bound by its instructions).
 //
 // Work: the K/V rows of a (row, KV head) -- a group -- are cut into tiles of
 // 16 KB of K and 16 KB of V; all groups' tiles form one list, and every CTA
-// (two per SM) takes an equal contiguous part of it, whatever the rows'
-// lengths are. A group that lies inside one CTA's part is written directly;
-// of any other, each CTA that holds a piece leaves (m, l, o) in the workspace,
-// and the last to arrive joins the pieces in their order (in two levels where
-// they are many).
+// (two or three per SM) takes an equal contiguous part of it, whatever the
+// rows' lengths are: with a fixed number of CTAs per group the longest row of a
+// ragged batch set the time. A part's ends move to a group's border where one
+// is near. A group that lies inside one CTA's part is written directly; of any
+// other, each CTA that holds a piece leaves (m, l, o) in the workspace, and the
+// last to arrive joins the pieces in their order (in two levels where they are
+// many). The counters end at zero.
 //
 // Inside a CTA a fifth warp walks the tiles ahead of the other four: it looks
-// their pages up and copies runs of up to 16 rows of a page by TMA into a ring
-// of three tiles, across the groups' borders. The four warps compute
-// S = Q K^T, each on a quarter of the tile's tokens, share the row maxima and
-// the weights through shared memory, and then O += P V, each on a quarter of
-// the head's coordinates: O is spread over the CTA and a group's end needs no
-// exchange, which keeps short rows cheap.
+// pages up (a batch of tiles ahead) and copies runs of up to 16 rows of a page
+// by TMA into a ring of two or three tiles, across the groups' borders. Sixteen
+// rows: bigger boxes for bigger pages gained nothing, and tiles may begin on
+// any box, so that little is copied that a window or a length leaves out. The
+// four warps compute S = Q K^T, each on a quarter of the tile's tokens, share
+// the row maxima and the weights through shared memory, and then O += P V, each
+// on a quarter of the head's coordinates: O is spread over the CTA and a
+// group's end needs no exchange, which keeps short rows cheap.
 #include "zha_paged.cuh"
 #include <type_traits>
 
@@ -37,14 +46,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4, kMath = kWarps * 32, kThreads = kMath + 32;
-constexpr int kStages = 3;
 constexpr int kRows = 16;                // query heads of a group, padded to the MMA's rows
 constexpr int kTileBytes = 16384;        // of K, and of V
-constexpr int kMaxWorkers = 148 * 2;
-constexpr int kMinTiles = 3;             // tiles of a CTA's part at least
+constexpr int kSms = 148, kMaxWorkers = kSms * 3;
+constexpr int kMinTiles = 3;             // tiles of a CTA's part at least (one row of 4,000 tokens: 13.7 us; 4: 15.3, 6: 17.5)
 constexpr int kBox = 16;                 // rows of a page copied at a time, at most
 constexpr int kDirect = 16;              // pieces of a group joined at once; more in two levels
-constexpr int kSnap = 2;                 // a CTA's part begins at a group's border if one is this near (in tiles)
+constexpr int kSnap = 2;                 // a CTA's part begins at a group's border if one is this near (in tiles; 1 and 3 are slower)
 constexpr long long kWaitCycles = 4000000000ll;   // ~2 s: a wait that long is an error
 
 // The tokens [lo, hi) that row r attends and the sequence they belong to
@@ -144,6 +152,9 @@ enum { kFirst = 1, kLast = 2, kHead = 4, kTail = 8, kEdge = 16 };
 template <typename T, int D, int GP>
 struct Shared {
     static constexpr bool kBf16 = sizeof(T) == 2;
+    // CTAs per SM and tiles in a CTA's ring. fp32 with few heads is bound by its instructions' latency: a third CTA
+    // hides more of it than a third tile (16 heads do not fit its registers).
+    static constexpr int kCtas = !kBf16 && GP == 8 ? 3 : 2, kStages = kCtas == 3 ? 2 : 3;
     static constexpr int TT = kTileBytes / (D * (int)sizeof(T));   // tokens of a tile
     static constexpr int ROWB = D * (int)sizeof(T), CH = ROWB / 16;       // bytes and 16-byte chunks of a row
     // K then V of a tile: blocks of 8 tokens, [ROWB / 128][8][128 bytes], 16-byte chunks XOR-swizzled by the row
@@ -330,8 +341,8 @@ __device__ __forceinline__ void math_bf16(const PagedAttnArgs &a, Shared<__nv_bf
 
     int seg = -1;
     for (int it = 0; it < n; ++it) {
-        const int st = it % kStages;
-        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
+        const int st = it % S::kStages;
+        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / S::kStages) & 1, kWaitCycles, abort, a.status);
         const Tile d = sm.tile[st];
         if (d.flags & kFirst) {
             ++seg;
@@ -569,8 +580,8 @@ __device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D
 
     int seg = -1;
     for (int it = 0; it < n; ++it) {
-        const int st = it % kStages;
-        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / kStages) & 1, kWaitCycles, abort, a.status);
+        const int st = it % S::kStages;
+        const bool ok = mbar_wait_bounded(smem_u32(&sm.full[st]), (it / S::kStages) & 1, kWaitCycles, abort, a.status);
         const Tile d = sm.tile[st];
         if (d.flags & kFirst) ++seg;
         const uint8_t *kt = sm.ring[st], *vt = kt + kTileBytes, *qp = sm.q[seg % S::QS][0];
@@ -771,7 +782,7 @@ __device__ __forceinline__ void math_f32(const PagedAttnArgs &a, Shared<float, D
 }
 
 template <typename T, int D, int GP, bool kTma>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shared<T, D, GP>::kCtas)
 paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   float *parts, int32_t *arrived) {
     using S = Shared<T, D, GP>;
@@ -783,7 +794,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     const int box = min(1 << a.lps, kBox);      // rows of a page copied at a time; tiles begin on a box
     volatile int *abort = &sm.abort;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < S::kStages; ++i) {
             mbar_init(smem_u32(&sm.full[i]), kTma ? 1 : 33);
             mbar_init(smem_u32(&sm.empty[i]), kWarps);
         }
@@ -1029,15 +1040,15 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             if (first && lane < a.G)
                 bulk_load(smem_u32(sm.q[seg % S::QS][lane]), static_cast<const T *>(a.q) + ((int64_t)t.r * a.Hq + t.kvh * a.G + lane) * D,
                           ROWB, full);
-            if (++st == kStages) {
+            if (++st == S::kStages) {
                 st = 0;
                 ++round;
             }
         }
         // given up: the copies in flight still land before the CTA may end
         if (k < n)
-            for (int j = k < kStages ? 0 : k - kStages; j < k; ++j)
-                mbar_wait_bounded(smem_u32(&sm.full[j % kStages]), (j / kStages) & 1, kWaitCycles, nullptr, a.status);
+            for (int j = k < S::kStages ? 0 : k - S::kStages; j < k; ++j)
+                mbar_wait_bounded(smem_u32(&sm.full[j % S::kStages]), (j / S::kStages) & 1, kWaitCycles, nullptr, a.status);
         return;
     }
 
@@ -1074,7 +1085,8 @@ bool pool_map(CUtensorMap *map, const void *pool, const PagedAttnArgs &a, int bo
 template <typename T, int D, int GP, bool kTma>
 cudaError_t launch(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaStream_t st) {
     const size_t smem = sizeof(Shared<T, D, GP>);
-    static_assert(2 * (sizeof(Shared<T, D, GP>) + 1024) <= 228 * 1024, "two CTAs per SM");
+    using S = Shared<T, D, GP>;
+    static_assert(S::kCtas * (sizeof(S) + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1092,7 +1104,7 @@ cudaError_t launch(const PagedAttnArgs &a, float *parts, int32_t *arrived, cudaS
     // no more CTAs than the longest possible rows would keep busy
     const int64_t longest = min64((int64_t)a.max_pages << a.lps, a.window > 0 ? (int64_t)a.window + kBox : INT64_MAX);
     const int64_t tiles = (longest + Shared<T, D, GP>::TT - 1) / Shared<T, D, GP>::TT * a.Hkv * a.rows;
-    const int grid = (int)max64(1, min64(kMaxWorkers, (tiles + kMinTiles - 1) / kMinTiles));
+    const int grid = (int)max64(1, min64(kSms * S::kCtas, (tiles + kMinTiles - 1) / kMinTiles));
     ProfScope ps("paged_decode", st);
     return launch_pdl(paged_attn_kernel<T, D, GP, kTma>, dim3(grid), dim3(kThreads), smem, st, a, kmap, vmap, parts, arrived);
 }
