@@ -1,4 +1,4 @@
-// zha_paged.cuh -- arguments of the paged-cache kernels and their launchers.
+// zha_paged.h -- arguments of the paged-cache kernels and their launchers.
 // Internal to libzha.
 #pragma once
 

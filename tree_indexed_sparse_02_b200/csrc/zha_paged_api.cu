@@ -3,7 +3,7 @@
 #include <limits.h>
 #include <math.h>
 
-#include "zha_paged.cuh"
+#include "zha_paged.h"
 
 namespace {
 

@@ -34,7 +34,7 @@
 // the row maxima and the weights through shared memory, and then O += P V, each
 // on a quarter of the head's coordinates: O is spread over the CTA and a
 // group's end needs no exchange, which keeps short rows cheap.
-#include "zha_paged.cuh"
+#include "zha_paged.h"
 #include <type_traits>
 
 #include "zha_tc.cuh"

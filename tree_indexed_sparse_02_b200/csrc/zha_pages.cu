@@ -13,7 +13,7 @@
 // with 8, 9.1 us with 16 (one CTA of an earlier form: 57 us).
 #include <cooperative_groups.h>
 
-#include "zha_paged.cuh"
+#include "zha_paged.h"
 
 namespace cg = cooperative_groups;
 

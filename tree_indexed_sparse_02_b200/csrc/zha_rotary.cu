@@ -12,7 +12,7 @@
 // pairs, so a lane turns the same coordinates of every head it meets: its
 // cosines and sines stay in registers, formed once per token by the whole warp
 // (one or two per lane, dealt out by shuffles).
-#include "zha_paged.cuh"
+#include "zha_paged.h"
 
 namespace zha {
 
