@@ -175,6 +175,20 @@ def test_binding_refuses_tensors_it_cannot_pass_on(zha):
             zha.paged_plan(cfg, **a)
 
 
+def test_binding_refuses_what_is_no_tensor(zha):
+    cfg = zha.paged_config(**BASE)
+    q = torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    for bad in (None, 5, [1.0], np.zeros((3, 8, 64)), torch.sparse_coo_tensor(size=(3, 8, 64))):
+        with pytest.raises(ValueError):
+            zha.paged_decode(cfg, bad, q, q, q, q, q, q)
+        with pytest.raises(ValueError):
+            zha.rotary(zha.Rotary(64, device="cpu"), bad, bad, q)
+        with pytest.raises(ValueError):
+            zha.paged_write(cfg, None, q, q, q, None, q, q, bad, q)
+        with pytest.raises(ValueError):
+            zha.paged_plan(cfg, bad, q, q, q, q, {"positions": q, "slots": q, "seq_ids": q, "cu": q})
+
+
 @pytest.mark.parametrize("rd", [2, 4, 34, 64, 128, 256])
 @pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 4.0), ("ntk", 8.0), ("yarn", 1.0), ("yarn", 16.0)])
 def test_rotary_frequencies(zha, rd, scaling, factor):

@@ -1,4 +1,5 @@
-"""Compile libzha.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc."""
+"""Compile libzha.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and _bind.so (argument marshalling of the
+paged and rotary calls, over torch's C++ headers) with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -6,11 +7,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libzha.so")
+BIND_SRC = os.path.join(CSRC, "zha_bind.cpp")
+BIND = os.path.join(HERE, "_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++20",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -40,7 +44,30 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    newest = max(os.path.getmtime(p) for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) > newest:
+        return BIND
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BIND + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE]
+    for inc in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", inc]
+    cmd += [BIND_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_bind(force, verbose)
     if not force and not _stale():
         return LIB
     objdir = os.path.join(HERE, "_build")

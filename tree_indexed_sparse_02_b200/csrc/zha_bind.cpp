@@ -1,0 +1,258 @@
+// zha_bind.cpp -- argument checks and marshalling of the paged-cache and
+// rotary calls for Python: tensors in, one call of the C ABI, its status out.
+//
+// These calls can take less time on the GPU than Python takes to look at their
+// tensors' attributes (8 us of host time with the checks in Python and ctypes,
+// of which the launch itself is 3), so the looking is done here, on the
+// tensors themselves. Nothing here computes or launches anything; the
+// functions of libzha.so are handed over by the binding (init). A call whose
+// tensors cannot be passed on raises ValueError and enqueues nothing.
+#include <Python.h>
+
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <stdexcept>
+#include <string>
+
+#include "zha.h"
+
+namespace {
+
+decltype(&zha_rotary_apply) f_rotary;
+decltype(&zha_paged_plan) f_plan;
+decltype(&zha_paged_write) f_write;
+decltype(&zha_paged_decode) f_decode;
+decltype(&zha_paged_workspace_bytes) f_workspace;
+
+struct Refused : std::runtime_error {
+    using std::runtime_error::runtime_error;
+};
+
+std::string list(at::IntArrayRef v) {
+    std::string s = "[";
+    for (size_t i = 0; i < v.size(); ++i) s += (i ? ", " : "") + std::to_string(v[i]);
+    return s + "]";
+}
+std::string shown(const at::Tensor &t) {
+    std::string s = std::string(", got ") + c10::toString(t.scalar_type()) + " " + list(t.sizes());
+    if (t.layout() == at::kStrided) s += " (strides " + list(t.strides()) + ")";
+    return s + " on " + t.device().str();
+}
+
+// One call's arguments: its name for messages, and the device that all its tensors must be on.
+struct Call {
+    const char *where;
+    int dev = -1;
+
+    [[noreturn]] void refuse(const std::string &what) const { throw Refused(std::string(where) + ": " + what); }
+    [[noreturn]] void refuse(const char *name, const std::string &what, const at::Tensor &t) const {
+        refuse(std::string(name) + " must be " + what + shown(t));
+    }
+
+    const at::Tensor &tensor(PyObject *o, const char *name) const {
+        if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
+        const at::Tensor &t = THPVariable_Unpack(o);
+        if (t.layout() != at::kStrided) refuse(name, "a strided tensor", t);
+        return t;
+    }
+    // [n, heads, d] with packed heads: its address and its tokens' stride in elements
+    void *rows(PyObject *o, const char *name, int64_t n, int64_t heads, int64_t d, at::ScalarType type, int64_t &stride) const {
+        const at::Tensor &t = tensor(o, name);
+        if (t.dim() != 3 || t.size(0) != n || t.size(1) != heads || t.size(2) != d || t.scalar_type() != type ||
+            t.get_device() != dev)
+            refuse(name, "[" + std::to_string(n) + ", " + std::to_string(heads) + ", " + std::to_string(d) + "] of the call's type on device " +
+                             std::to_string(dev), t);
+        if (n > 0 && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != d))) refuse(name, "a tensor whose heads are packed", t);
+        stride = n > 1 ? t.stride(0) : heads * d;
+        return t.data_ptr();
+    }
+    // contiguous, of at least (or exactly) n elements
+    void *block(PyObject *o, const char *name, int64_t n, at::ScalarType type, bool exact) const {
+        const at::Tensor &t = tensor(o, name);
+        if (t.scalar_type() != type || t.get_device() != dev || !t.is_contiguous() || (exact ? t.numel() != n : t.numel() < n))
+            refuse(name, std::string("a contiguous ") + c10::toString(type) + " tensor of " + (exact ? "" : "at least ") +
+                             std::to_string(n) + " elements on device " + std::to_string(dev), t);
+        return t.data_ptr();
+    }
+    int32_t *ints(PyObject *o, const char *name, int64_t n) const {      // None passes
+        return o == Py_None ? nullptr : static_cast<int32_t *>(block(o, name, n, at::kInt, false));
+    }
+    void on(const at::Tensor &t) {
+        dev = t.get_device();
+        if (!t.is_cuda()) refuse("tensors must be on a CUDA device" + shown(t));
+    }
+    void *stream(PyObject *o) const {
+        if (o != Py_None) return PyLong_AsVoidPtr(o);
+        return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+    }
+};
+
+at::ScalarType type_of(const zha_paged_config *c) { return c->dtype == ZHA_BF16 ? at::kBFloat16 : at::kFloat; }
+int64_t pool_elements(const zha_paged_config *c) {
+    return (int64_t)c->n_pages * c->n_kv_heads * c->page_size * c->head_dim;
+}
+const zha_paged_config *config(PyObject *o) { return static_cast<const zha_paged_config *>(PyLong_AsVoidPtr(o)); }
+
+// The rotation's description (an address, or None) and the device its table is on.
+const zha_rotary *rotation(const Call &c, PyObject *o, PyObject *device) {
+    if (o == Py_None) return nullptr;
+    if (PyLong_AsLong(device) != c.dev) c.refuse("the rotary table is on another device than the tensors");
+    return static_cast<const zha_rotary *>(PyLong_AsVoidPtr(o));
+}
+
+template <typename F>
+PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
+    if (n != want) {
+        PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+        return nullptr;
+    }
+    try {
+        const int code = f();
+        return PyErr_Occurred() ? nullptr : PyLong_FromLong(code);
+    } catch (const Refused &e) {
+        PyErr_SetString(PyExc_ValueError, e.what());
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    }
+    return nullptr;
+}
+
+// rotary, its device, q, k, positions, q_out, k_out, transpose, stream
+PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&] {
+        Call c{"zha_rotary_apply"};
+        const bool has_q = a[2] != Py_None, has_k = a[3] != Py_None;
+        if (!has_q && !has_k) c.refuse("q or k [n, heads, d] is needed");
+        const at::Tensor &one = c.tensor(has_q ? a[2] : a[3], has_q ? "q" : "k");
+        if (one.dim() != 3) c.refuse(has_q ? "q" : "k", "[n, heads, d]", one);
+        c.on(one);
+        const auto type = one.scalar_type();
+        if (type != at::kBFloat16 && type != at::kFloat) c.refuse(has_q ? "q" : "k", "bf16 or fp32", one);
+        const int64_t tokens = one.size(0), d = one.size(2), hq = has_q ? one.size(1) : 0;
+        if (tokens > INT32_MAX || d > INT32_MAX || one.size(1) > INT32_MAX) c.refuse("too large");
+        int64_t hk = 0, qs = 0, qos = 0, ks = 0, kos = 0;
+        void *qp = nullptr, *qo = nullptr, *kp = nullptr, *ko = nullptr;
+        if (has_q) {
+            qp = c.rows(a[2], "q", tokens, hq, d, type, qs);
+            qo = a[5] == Py_None ? (qos = qs, qp) : c.rows(a[5], "q_out", tokens, hq, d, type, qos);
+        }
+        if (has_k) {
+            const at::Tensor &k = c.tensor(a[3], "k");
+            hk = k.dim() == 3 ? k.size(1) : 0;
+            kp = c.rows(a[3], "k", tokens, hk, d, type, ks);
+            ko = a[6] == Py_None ? (kos = ks, kp) : c.rows(a[6], "k_out", tokens, hk, d, type, kos);
+        }
+        const int32_t *pos = c.ints(a[4], "positions", tokens);
+        const zha_rotary *r = rotation(c, a[0], a[1]);
+        c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+        return (int)f_rotary(r, (int32_t)d, type == at::kFloat ? ZHA_F32 : ZHA_BF16, (int32_t)tokens, (int32_t)hq, (int32_t)hk,
+                             qp, qs, kp, ks, pos, qo, qos, ko, kos, PyObject_IsTrue(a[7]) == 1, c.stream(a[8]));
+    });
+}
+
+// config, table, lens, n_new, free_pages, n_free, positions, slots, seq_ids, cu, lens_out, n_free_out, status, stream
+PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        Call c{"zha_paged_plan"};
+        const zha_paged_config *cfg = config(a[0]);
+        c.on(c.tensor(a[1], "table"));
+        const int64_t B = cfg->batch, rows = c.tensor(a[7], "slots").numel();
+        if (rows > INT32_MAX) c.refuse("the token buffer is too large");
+        zha_token_map m{};
+        m.positions = c.ints(a[6], "positions", rows);
+        m.slots = c.ints(a[7], "slots", rows);
+        m.seq_ids = c.ints(a[8], "seq_ids", rows);
+        m.cu_new = c.ints(a[9], "cu", B + 1);
+        m.max_tokens = (int32_t)rows;
+        int32_t *lens = c.ints(a[2], "lens", B), *n_free = c.ints(a[5], "n_free", 1);
+        int32_t *lens_out = a[10] == Py_None ? lens : c.ints(a[10], "lens_out", B);
+        int32_t *n_free_out = a[11] == Py_None ? n_free : c.ints(a[11], "n_free_out", 1);
+        int32_t *table = c.ints(a[1], "table", B * cfg->max_pages);
+        const int32_t *n_new = c.ints(a[3], "n_new", B);
+        int32_t *free_pages = c.ints(a[4], "free_pages", cfg->n_pages), *status = c.ints(a[12], "dev_status", 1);
+        c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+        return (int)f_plan(cfg, table, lens, n_new, free_pages, n_free, lens_out, n_free_out, &m, status, c.stream(a[13]));
+    });
+}
+
+// config, rotary, its device, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, status, stream
+PyObject *paged_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 13, [&] {
+        Call c{"zha_paged_write"};
+        const zha_paged_config *cfg = config(a[0]);
+        c.on(c.tensor(a[9], "k_pool"));
+        const auto type = type_of(cfg);
+        const int64_t d = cfg->head_dim, hkv = cfg->n_kv_heads, hq = cfg->n_q_heads, size = pool_elements(cfg);
+        const at::Tensor &k = c.tensor(a[4], "k_new");
+        const int64_t tokens = k.dim() ? k.size(0) : 0;
+        if (tokens > INT32_MAX) c.refuse("too many tokens");
+        int64_t qs = 0, ks = 0, vs = 0;
+        const void *kp = c.rows(a[4], "k_new", tokens, hkv, d, type, ks), *vp = c.rows(a[5], "v_new", tokens, hkv, d, type, vs);
+        void *qp = nullptr, *qo = nullptr;
+        if (a[3] != Py_None) {
+            qp = c.rows(a[3], "q", tokens, hq, d, type, qs);
+            if (a[8] == Py_None) c.refuse("q_out is needed with q");
+            qo = c.block(a[8], "q_out", tokens * hq * d, type, true);
+        }
+        const int32_t *pos = c.ints(a[6], "positions", tokens), *slots = c.ints(a[7], "slots", tokens);
+        void *k_pool = c.block(a[9], "k_pool", size, type, true), *v_pool = c.block(a[10], "v_pool", size, type, true);
+        int32_t *status = c.ints(a[11], "dev_status", 1);
+        const zha_rotary *r = rotation(c, a[1], a[2]);
+        c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+        return (int)f_write(cfg, r, (int32_t)tokens, qp, qs, kp, ks, vp, vs, pos, slots, qo, k_pool, v_pool, status,
+                            c.stream(a[12]));
+    });
+}
+
+// config, q, k_pool, v_pool, table, lens, out, workspace, lse, seq_ids, positions, status, stream
+PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 13, [&] {
+        Call c{"zha_paged_decode"};
+        const zha_paged_config *cfg = config(a[0]);
+        const at::Tensor &q = c.tensor(a[1], "q");
+        c.on(q);
+        const auto type = type_of(cfg);
+        const int64_t d = cfg->head_dim, hq = cfg->n_q_heads, B = cfg->batch, size = pool_elements(cfg);
+        const int64_t rows = q.dim() == 3 ? q.size(0) : -1;
+        if (rows < 0 || rows > INT32_MAX || q.size(1) != hq || q.size(2) != d)
+            c.refuse("q", "[n, " + std::to_string(hq) + ", " + std::to_string(d) + "]", q);
+        if (a[9] == Py_None && rows > B) c.refuse("q", "of no more rows than sequences where seq_ids is not given", q);
+        void *qp = c.block(a[1], "q", rows * hq * d, type, true), *out = c.block(a[6], "out", rows * hq * d, type, true);
+        float *lse = a[8] == Py_None ? nullptr : static_cast<float *>(c.block(a[8], "lse", rows * hq, at::kFloat, true));
+        const at::Tensor &ws = c.tensor(a[7], "workspace");
+        const size_t need = rows ? f_workspace(cfg, (int32_t)rows) : 0;
+        if (ws.get_device() != c.dev || !ws.is_contiguous() || ws.nbytes() < need)
+            c.refuse("workspace", "contiguous, on the call's device and of at least " + std::to_string(need) + " bytes", ws);
+        const void *k_pool = c.block(a[2], "k_pool", size, type, true), *v_pool = c.block(a[3], "v_pool", size, type, true);
+        const int32_t *table = c.ints(a[4], "table", B * cfg->max_pages), *lens = c.ints(a[5], "lens", B);
+        const int32_t *seq = c.ints(a[9], "seq_ids", rows), *pos = c.ints(a[10], "positions", rows);
+        int32_t *status = c.ints(a[11], "dev_status", 1);
+        c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+        return (int)f_decode(cfg, (int32_t)rows, qp, k_pool, v_pool, table, lens, seq, pos, out, lse, ws.data_ptr(), status,
+                             c.stream(a[12]));
+    });
+}
+
+// Addresses of libzha.so's functions: rotary_apply, paged_plan, paged_write, paged_decode, paged_workspace_bytes.
+PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        f_rotary = reinterpret_cast<decltype(f_rotary)>(PyLong_AsVoidPtr(a[0]));
+        f_plan = reinterpret_cast<decltype(f_plan)>(PyLong_AsVoidPtr(a[1]));
+        f_write = reinterpret_cast<decltype(f_write)>(PyLong_AsVoidPtr(a[2]));
+        f_decode = reinterpret_cast<decltype(f_decode)>(PyLong_AsVoidPtr(a[3]));
+        f_workspace = reinterpret_cast<decltype(f_workspace)>(PyLong_AsVoidPtr(a[4]));
+        return 0;
+    });
+}
+
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {FAST(init), FAST(rotary), FAST(paged_plan), FAST(paged_write), FAST(paged_decode), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&module); }

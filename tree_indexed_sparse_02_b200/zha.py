@@ -3,7 +3,8 @@
 Argument marshalling only: every function forwards device pointers of torch
 tensors and a CUDA stream to the library, and raises ``ZhaError`` on a
 non-zero status. Nothing here computes any step of the method; if libzha.so
-is missing the import fails loudly (there is no fallback path).
+(or _bind.so, the marshalling of the paged and rotary calls) is missing the
+import fails loudly (there is no fallback path).
 """
 from __future__ import annotations
 
@@ -12,6 +13,11 @@ import functools
 import os
 
 import torch
+
+try:
+    from . import _bind
+except ImportError as e:
+    raise ImportError(f"_bind.so not built or not loadable ({e}); run tree_indexed_sparse_02_b200/build.py") from e
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzha.so")
@@ -26,7 +32,6 @@ ZHA_SUMMARY_NATIVE, ZHA_SUMMARY_MXFP8 = 0, 1
 ZHA_ROPE_HALF, ZHA_ROPE_INTERLEAVED = 0, 1
 ZHA_ROPE_PLAIN, ZHA_ROPE_LINEAR, ZHA_ROPE_NTK, ZHA_ROPE_YARN = 0, 1, 2, 3
 ZHA_MAX_LEVELS = 8
-_DTYPES = {torch.bfloat16: ZHA_BF16, torch.float32: ZHA_F32}
 STATUS_NAMES = {0: "ZHA_OK", 1: "ZHA_ERR_INVALID_ARG", 2: "ZHA_ERR_UNSUPPORTED",
                 3: "ZHA_ERR_CAPACITY", 4: "ZHA_ERR_CUDA", 5: "ZHA_ERR_TIMEOUT"}
 
@@ -69,25 +74,13 @@ class PagedConfig(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("window", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
 
-    # What the calls need of a configuration every time, made once (a configuration is not changed after its first
-    # call: make another).
     @functools.cached_property
     def torch_dtype(self):
         return torch.bfloat16 if self.dtype == ZHA_BF16 else torch.float32
 
     @functools.cached_property
-    def ref(self):
-        return ctypes.byref(self)
-
-    @functools.cached_property
-    def pool_elements(self):
-        return self.n_pages * self.n_kv_heads * self.page_size * self.head_dim
-
-    def decode_workspace(self, rows):
-        known = self.__dict__.setdefault("_workspace", {})
-        if rows not in known:
-            known[rows] = int(_lib.zha_paged_workspace_bytes(self.ref, rows)) if rows else 0
-        return known[rows]
+    def address(self):
+        return ctypes.addressof(self)
 
 
 class TokenMap(ctypes.Structure):
@@ -151,8 +144,9 @@ def _load():
 
 
 _lib = _load()
-_rotary_apply, _paged_plan = _lib.zha_rotary_apply, _lib.zha_paged_plan
-_paged_write, _paged_decode = _lib.zha_paged_write, _lib.zha_paged_decode
+_bind.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
+             for name in ("zha_rotary_apply", "zha_paged_plan", "zha_paged_write", "zha_paged_decode",
+                          "zha_paged_workspace_bytes")))
 
 
 def lib():
@@ -309,55 +303,6 @@ def paged_workspace(cfg: PagedConfig, rows: int, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-# The checks below are on the path of every call, whose kernels can take less time than their launch: they read
-# few tensor attributes, and the messages are made only where one fails. `dev` is a device index (-1: not CUDA).
-
-def _refuse(where: str, what: str, t=None):
-    got = "" if t is None else f", got {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}"
-    raise ValueError(f"{where}: {what}{got}")
-
-
-def _rows(t, where, name, n, heads, d, dtype, dev):
-    """The address and the token stride (elements) of a [n, heads, d] tensor whose heads are packed; any other layout
-    is refused."""
-    if t.shape != (n, heads, d) or t.dtype is not dtype or t.get_device() != dev:
-        _refuse(where, f"{name} must be a {dtype} tensor [{n}, {heads}, {d}] on device {dev}", t)
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 or (s1 != d and heads > 1)) and n > 0:
-        _refuse(where, f"{name}'s heads must be packed", t)
-    return t.data_ptr(), s0 if n > 1 else heads * d
-
-
-def _int32(t, where, name, n, dev):
-    """The address of an int32 array of at least n entries; None passes."""
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
-        _refuse(where, f"{name} must be a contiguous int32 tensor of at least {n} entries on device {dev}", t)
-    return t.data_ptr()
-
-
-def _block(t, where, name, n, dtype, dev):
-    """The address of a contiguous array of n elements."""
-    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
-        _refuse(where, f"{name} must be a contiguous {dtype} tensor of {n} elements on device {dev}", t)
-    return t.data_ptr()
-
-
-def _call(where, fn, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current, on its current stream by default."""
-    if dev < 0:
-        _refuse(where, "tensors must be on a CUDA device")
-    here = torch._C._cuda_getDevice()
-    if dev != here:
-        with torch.cuda.device(dev):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-    else:
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-    if code != 0:
-        raise ZhaError(code, where)
-
-
 class Rotary:
     """A rotary embedding: its frequency table (turns per position, fp64) on the device.
 
@@ -374,42 +319,21 @@ class Rotary:
                                     int(original_len), table, ctypes.byref(m)), "zha_rotary_freqs")
         self.freq = torch.tensor(list(table), dtype=torch.float64).to(device)
         self.desc = RotaryDesc(int(rotary_dim), lay.get(layout, layout), m.value, 0, self.freq.data_ptr())
-        self.ref = ctypes.byref(self.desc)
+        self.address = ctypes.addressof(self.desc)
         self.device = self.freq.get_device()
 
+
+# The calls below check their tensors (type, shape, layout, device: ValueError) and pass them on in csrc/zha_bind.cpp:
+# on the GPU they can take less time than Python takes to look at the tensors' attributes.
 
 def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
     """Rotate q [n, Hq, d] and k [n, Hk, d] (either may be None; tokens may be strided) at int32 positions [n].
     The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out)."""
-    where = "zha_rotary_apply"
-    one = k if q is None else q
-    if one is None or one.ndim != 3:
-        _refuse(where, "q or k [n, heads, d] is needed", one)
-    (n, heads, d), dt, dev = one.shape, one.dtype, one.get_device()
-    code = _DTYPES.get(dt)
-    if code is None:
-        _refuse(where, "bf16 or fp32 is needed", one)
-    hq = hk = qs = ks = qos = kos = 0
-    qp = kp = qo = ko = None
-    if q is not None:
-        hq = heads
-        qp, qs = _rows(q, where, "q", n, hq, d, dt, dev)
-        if q_out is None:
-            q_out, qo, qos = q, qp, qs
-        else:
-            qo, qos = _rows(q_out, where, "q_out", n, hq, d, dt, dev)
-    if k is not None:
-        hk = k.shape[1] if k.ndim == 3 else 0
-        kp, ks = _rows(k, where, "k", n, hk, d, dt, dev)
-        if k_out is None:
-            k_out, ko, kos = k, kp, ks
-        else:
-            ko, kos = _rows(k_out, where, "k_out", n, hk, d, dt, dev)
-    if rot.device != dev:
-        _refuse(where, f"the rotary table is on device {rot.device}, the tensors on {dev}")
-    _call(where, _rotary_apply, dev, stream, rot.ref, d, code, n, hq, hk, qp, qs, kp, ks,
-          _int32(positions, where, "positions", n, dev), qo, qos, ko, kos, 1 if transpose else 0)
-    return q_out, k_out
+    code = _bind.rotary(rot.address, rot.device, q, k, positions, q_out, k_out, transpose,
+                        None if stream is None else stream.cuda_stream)
+    if code:
+        raise ZhaError(code, "zha_rotary_apply")
+    return q if q_out is None else q_out, k if k_out is None else k_out
 
 
 def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_map, lens_out=None, n_free_out=None,
@@ -417,42 +341,22 @@ def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_m
     """Block tables, slots and lengths of a step with n_new[b] new tokens of sequence b (< 0: it ends).
     token_map: {"positions", "slots", "seq_ids"} (one entry per row of the token buffer) and "cu" [batch + 1];
     lens_out and n_free_out default to lens and n_free (in place)."""
-    where, dev, B = "zha_paged_plan", table.get_device(), cfg.batch
-    slots = token_map["slots"]
-    rows = slots.numel()
-    m = TokenMap(_int32(token_map["positions"], where, "positions", rows, dev), _int32(slots, where, "slots", rows, dev),
-                 _int32(token_map["seq_ids"], where, "seq_ids", rows, dev),
-                 _int32(token_map["cu"], where, "cu", B + 1, dev), rows, 0)
-    lens_p, free_p = _int32(lens, where, "lens", B, dev), _int32(n_free, where, "n_free", 1, dev)
-    _call(where, _paged_plan, dev, stream, cfg.ref, _int32(table, where, "table", B * cfg.max_pages, dev),
-          lens_p, _int32(n_new, where, "n_new", B, dev), _int32(free_pages, where, "free_pages", cfg.n_pages, dev), free_p,
-          lens_p if lens_out is None else _int32(lens_out, where, "lens_out", B, dev),
-          free_p if n_free_out is None else _int32(n_free_out, where, "n_free_out", 1, dev), ctypes.byref(m),
-          _int32(dev_status, where, "dev_status", 1, dev))
+    m = token_map
+    code = _bind.paged_plan(cfg.address, table, lens, n_new, free_pages, n_free, m["positions"], m["slots"], m["seq_ids"],
+                            m["cu"], lens_out, n_free_out, dev_status, None if stream is None else stream.cuda_stream)
+    if code:
+        raise ZhaError(code, "zha_paged_plan")
 
 
 def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status=None,
                 stream=None):
     """Rotate q and k_new [n, heads, d] and write k_new, v_new to their cache slots [n] (negative: skipped).
     rot None: no rotation; q None: keys and values only."""
-    where, dev, dt, d, hkv = "zha_paged_write", k_pool.get_device(), cfg.torch_dtype, cfg.head_dim, cfg.n_kv_heads
-    n = k_new.shape[0]
-    kp, ks = _rows(k_new, where, "k_new", n, hkv, d, dt, dev)
-    vp, vs = _rows(v_new, where, "v_new", n, hkv, d, dt, dev)
-    qs, qp, qo = 0, None, None
-    if q is not None:
-        hq = cfg.n_q_heads
-        qp, qs = _rows(q, where, "q", n, hq, d, dt, dev)
-        if q_out is None:
-            _refuse(where, "q_out is needed with q")
-        qo = _block(q_out, where, "q_out", n * hq * d, dt, dev)
-    if rot is not None and rot.device != dev:
-        _refuse(where, f"the rotary table is on device {rot.device}, the tensors on {dev}")
-    size = cfg.pool_elements
-    _call(where, _paged_write, dev, stream, cfg.ref, None if rot is None else rot.ref, n, qp, qs, kp, ks, vp, vs,
-          _int32(positions, where, "positions", n, dev), _int32(slots, where, "slots", n, dev), qo,
-          _block(k_pool, where, "k_pool", size, dt, dev), _block(v_pool, where, "v_pool", size, dt, dev),
-          _int32(dev_status, where, "dev_status", 1, dev))
+    code = _bind.paged_write(cfg.address, None if rot is None else rot.address, None if rot is None else rot.device, q, k_new,
+                             v_new, positions, slots, q_out, k_pool, v_pool, dev_status,
+                             None if stream is None else stream.cuda_stream)
+    if code:
+        raise ZhaError(code, "zha_paged_write")
     return q_out
 
 
@@ -460,20 +364,10 @@ def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspac
                  positions=None, dev_status=None, stream=None):
     """Attention of rows q [n, Hq, d] over the paged cache into out (and lse [n, Hq] fp32). Row r is of sequence
     seq_ids[r] (default r; negative: left as it is) and attends tokens 0 .. positions[r] (default: all)."""
-    where, dev, dt, hq, d = "zha_paged_decode", q.get_device(), cfg.torch_dtype, cfg.n_q_heads, cfg.head_dim
-    n, size, batch = q.shape[0], cfg.pool_elements, cfg.batch
-    if q.ndim != 3 or (seq_ids is None and n > batch):
-        _refuse(where, f"q must be [n, {hq}, {d}] with a sequence for each row", q)
-    qp, op = _block(q, where, "q", n * hq * d, dt, dev), _block(out, where, "out", n * hq * d, dt, dev)
-    if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < cfg.decode_workspace(n):
-        _refuse(where, f"the workspace must be contiguous and hold paged_workspace_bytes(cfg, {n}) bytes on device {dev}",
-                workspace)
-    _call(where, _paged_decode, dev, stream, cfg.ref, n, qp,
-          _block(k_pool, where, "k_pool", size, dt, dev), _block(v_pool, where, "v_pool", size, dt, dev),
-          _int32(table, where, "table", batch * cfg.max_pages, dev), _int32(lens, where, "lens", batch, dev),
-          _int32(seq_ids, where, "seq_ids", n, dev), _int32(positions, where, "positions", n, dev), op,
-          None if lse is None else _block(lse, where, "lse", n * hq, torch.float32, dev), workspace.data_ptr(),
-          _int32(dev_status, where, "dev_status", 1, dev))
+    code = _bind.paged_decode(cfg.address, q, k_pool, v_pool, table, lens, out, workspace, lse, seq_ids, positions,
+                              dev_status, None if stream is None else stream.cuda_stream)
+    if code:
+        raise ZhaError(code, "zha_paged_decode")
     return out
 
 
