@@ -138,3 +138,27 @@ def test_decode_graph_rotates_while_staging(zha):
         buf.check_status()
         outs.append((torch.stack(got), inp.K.clone()))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_copies_of_handles_stand_alone(zha):
+    """A deep copy of a Rotary or of a configuration works after the original is gone."""
+    import copy
+    import gc
+    x = torch.randn(5, 2, 64, generator=torch.Generator().manual_seed(4)).cuda()
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    rot = zha.Rotary(64)
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    zha.rotary(rot, x, None, pos, want)
+    twin = copy.deepcopy(rot)
+    rot.freq.zero_()
+    del rot
+    gc.collect()
+    zha.rotary(twin, x, None, pos, got)
+    assert torch.equal(got, want)
+    cfg = zha.paged_config(1, 2, 1, 64, 16, 4, 4, dtype="f32")
+    other = copy.copy(cfg)
+    del cfg
+    gc.collect()
+    k = torch.zeros(4, 1, 16, 64, device="cuda")
+    zha.paged_write(other, None, None, x[:, :1].contiguous(), x[:, 1:].contiguous(), None, pos, None, k, k.clone())
+    assert torch.equal(k[0, 0, :5], x[:, 0])

@@ -8,8 +8,8 @@ import fails loudly (there is no fallback path).
 """
 from __future__ import annotations
 
+import copy
 import ctypes
-import functools
 import os
 
 import torch
@@ -74,13 +74,9 @@ class PagedConfig(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("window", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
 
-    @functools.cached_property
+    @property
     def torch_dtype(self):
         return torch.bfloat16 if self.dtype == ZHA_BF16 else torch.float32
-
-    @functools.cached_property
-    def address(self):
-        return ctypes.addressof(self)
 
 
 class TokenMap(ctypes.Structure):
@@ -319,8 +315,18 @@ class Rotary:
                                     int(original_len), table, ctypes.byref(m)), "zha_rotary_freqs")
         self.freq = torch.tensor(list(table), dtype=torch.float64).to(device)
         self.desc = RotaryDesc(int(rotary_dim), lay.get(layout, layout), m.value, 0, self.freq.data_ptr())
-        self.address = ctypes.addressof(self.desc)
         self.device = self.freq.get_device()
+
+    @property
+    def address(self):
+        return ctypes.addressof(self.desc)
+
+    def __deepcopy__(self, memo):
+        twin = copy.copy(self)
+        twin.freq = self.freq.clone()
+        d = self.desc
+        twin.desc = RotaryDesc(d.rotary_dim, d.layout, d.mscale, 0, twin.freq.data_ptr())
+        return twin
 
 
 # The calls below check their tensors (type, shape, layout, device: ValueError) and pass them on in csrc/zha_bind.cpp:
@@ -342,7 +348,7 @@ def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_m
     token_map: {"positions", "slots", "seq_ids"} (one entry per row of the token buffer) and "cu" [batch + 1];
     lens_out and n_free_out default to lens and n_free (in place)."""
     m = token_map
-    code = _bind.paged_plan(cfg.address, table, lens, n_new, free_pages, n_free, m["positions"], m["slots"], m["seq_ids"],
+    code = _bind.paged_plan(ctypes.addressof(cfg), table, lens, n_new, free_pages, n_free, m["positions"], m["slots"], m["seq_ids"],
                             m["cu"], lens_out, n_free_out, dev_status, None if stream is None else stream.cuda_stream)
     if code:
         raise ZhaError(code, "zha_paged_plan")
@@ -352,7 +358,7 @@ def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out,
                 stream=None):
     """Rotate q and k_new [n, heads, d] and write k_new, v_new to their cache slots [n] (negative: skipped).
     rot None: no rotation; q None: keys and values only."""
-    code = _bind.paged_write(cfg.address, None if rot is None else rot.address, None if rot is None else rot.device, q, k_new,
+    code = _bind.paged_write(ctypes.addressof(cfg), None if rot is None else rot.address, None if rot is None else rot.device, q, k_new,
                              v_new, positions, slots, q_out, k_pool, v_pool, dev_status,
                              None if stream is None else stream.cuda_stream)
     if code:
@@ -364,7 +370,7 @@ def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspac
                  positions=None, dev_status=None, stream=None):
     """Attention of rows q [n, Hq, d] over the paged cache into out (and lse [n, Hq] fp32). Row r is of sequence
     seq_ids[r] (default r; negative: left as it is) and attends tokens 0 .. positions[r] (default: all)."""
-    code = _bind.paged_decode(cfg.address, q, k_pool, v_pool, table, lens, out, workspace, lse, seq_ids, positions,
+    code = _bind.paged_decode(ctypes.addressof(cfg), q, k_pool, v_pool, table, lens, out, workspace, lse, seq_ids, positions,
                               dev_status, None if stream is None else stream.cuda_stream)
     if code:
         raise ZhaError(code, "zha_paged_decode")
