@@ -272,6 +272,18 @@ def test_decode_edge_lengths(zha, dt, d, hq, hkv, page):
 
 
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page", [2, 4, 8, 32, 64, 256, 1024])
+def test_decode_page_sizes(zha, dt, page):
+    """Every way of copying pages: row by row, whole small pages, parts of large ones; with a window that begins
+    inside them, and garbage in the rows around it."""
+    lens = [1, 7, 9, 100, 1023, 1025, 2500]
+    for window in (0, 77):
+        c = Case(zha, lens, 12, 4, 128, page, dt, window=window, seed=page)
+        q = c.queries(len(lens))
+        c.check(q, *c.run(q), [(b, b, n) for b, n in enumerate(lens)])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("lens", [[5000], [20011, 3], [777] * 40, [1] * 300, [4097, 0, 0, 9000, 1, 64]],
                          ids=["one", "long+short", "even", "ones", "ragged"])
 def test_decode_splits_and_joins(zha, dt, lens):
