@@ -162,3 +162,26 @@ def test_copies_of_handles_stand_alone(zha):
     k = torch.zeros(4, 1, 16, 64, device="cuda")
     zha.paged_write(other, None, None, x[:, :1].contiguous(), x[:, 1:].contiguous(), None, pos, None, k, k.clone())
     assert torch.equal(k[0, 0, :5], x[:, 0])
+
+
+@pytest.mark.parametrize("stride", [0, 64])
+def test_overlapping_tokens_are_refused(zha, stride):
+    """A broadcast token (stride 0, which the C call takes for contiguous) or tokens that share coordinates."""
+    n, h, d = 6, 2, 64
+    one = torch.zeros(n + 1, h, d, dtype=torch.bfloat16, device="cuda")
+    odd = one.as_strided((n, h, d), (stride, d, 1))
+    whole = one[:n].clone()
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    rot = zha.Rotary(d)
+    for kw in (dict(q=odd, q_out=whole), dict(k=odd, k_out=whole), dict(q=odd), dict(q=whole, q_out=odd),
+               dict(k=whole, k_out=odd)):
+        with pytest.raises(ValueError, match="overlap"):
+            zha.rotary(rot, kw.pop("q", None), kw.pop("k", None), ids, **kw)
+    cfg = zha.paged_config(1, h, h, d, 16, 1, 1)
+    pool = torch.zeros(1, h, 16, d, dtype=torch.bfloat16, device="cuda")
+    for q, k, v in ((odd, whole, whole), (whole, odd, whole), (whole, whole, odd)):
+        with pytest.raises(ValueError, match="overlap"):
+            zha.paged_write(cfg, rot, q, k, v, ids, ids, whole, pool, pool)
+    # one token alone overlaps nothing, whatever its stride
+    zha.rotary(rot, odd[:1], None, ids)
+    torch.cuda.synchronize()

@@ -65,6 +65,8 @@ struct Call {
             refuse(name, "[" + std::to_string(n) + ", " + std::to_string(heads) + ", " + std::to_string(d) + "] of the call's type on device " +
                              std::to_string(dev), t);
         if (n > 0 && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != d))) refuse(name, "a tensor whose heads are packed", t);
+        // (a stride of 0 is a broadcast here, and contiguous in the C call)
+        if (n > 1 && t.stride(0) < heads * d) refuse(name, "a tensor whose tokens do not overlap", t);
         stride = n > 1 ? t.stride(0) : heads * d;
         return t.data_ptr();
     }
