@@ -523,7 +523,8 @@ ZHA_API zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary
 /* Bytes of scratch zha_paged_decode needs for up to n_rows rows. Zero it once
  * before its first use: every call leaves its counters at zero again. One
  * workspace serves one call at a time (calls that can overlap on the GPU, and
- * graphs that can, need one each). 0 for a bad config or n_rows < 1. */
+ * graphs that can, need one each); calls of different configurations may share
+ * one that is large enough for each. 0 for a bad config or n_rows < 1. */
 ZHA_API size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_rows);
 
 /*

@@ -477,6 +477,17 @@ def test_decode_many_rows_and_one_workspace(zha):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+def test_decode_configurations_share_a_workspace(zha):
+    """Calls of different types, heads and head sizes, all with split rows, one after the other on one workspace."""
+    lens = [20000, 5, 7001]
+    cases = [Case(zha, lens, hq, hkv, d, 16, dt, seed=30 + i)
+             for i, (hq, hkv, d, dt) in enumerate([(16, 1, 128, BF16), (2, 2, 64, BF16), (3, 1, 64, F32), (8, 1, 128, F32)])]
+    ws = max((zha.paged_workspace(c.cfg, 3) for c in cases), key=lambda t: t.numel())
+    for c in cases + cases:
+        q = c.queries(3)
+        c.check(q, *c.run(q, ws), [(0, 0, lens[0]), (1, 1, lens[1]), (2, 2, lens[2])])
+
+
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 def test_empty_calls_and_queries_in_place(zha, dt):
     cfg = zha.paged_config(2, 4, 2, 64, 16, 6, 3, dtype=NAME[dt])

@@ -1126,12 +1126,16 @@ size_t pieces_bytes(const PagedAttnArgs &a) { return (size_t)kMaxWorkers * 2 * p
 
 }  // namespace
 
-// Two pieces per CTA, then a counter per piece for sets and one for groups.
-size_t paged_attn_workspace(const PagedAttnArgs &a) { return pieces_bytes(a) + 4 * kMaxWorkers * sizeof(int32_t); }
+// A counter per piece for sets and one for groups, then two pieces per CTA. (The counters come first: their place
+// is the same for all configurations, so that one workspace serves several.)
+constexpr size_t kCounterBytes = 4 * kMaxWorkers * sizeof(int32_t);
+static_assert(kCounterBytes % 16 == 0, "pieces are whole float4s");
+
+size_t paged_attn_workspace(const PagedAttnArgs &a) { return kCounterBytes + pieces_bytes(a); }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, cudaStream_t st) {
-    float *parts = static_cast<float *>(a.ws);
-    int32_t *arrived = reinterpret_cast<int32_t *>(static_cast<char *>(a.ws) + pieces_bytes(a));
+    int32_t *arrived = static_cast<int32_t *>(a.ws);
+    float *parts = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kCounterBytes);
     return a.d == 128 ? launch_dim<128>(a, parts, arrived, st) : launch_dim<64>(a, parts, arrived, st);
 }
 
