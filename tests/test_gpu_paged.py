@@ -568,3 +568,22 @@ def test_steps_of_the_whole_cache(zha, dt, captured):
                 i += 1
         assert torch.all(cache.out[i:] == 77)                         # padding rows are left as they were
         assert cache.lens.tolist() == [len(h[0]) for h in hist]
+
+
+def test_tables_of_another_width_are_refused(zha):
+    """Wider or narrower rows than the configuration's max_pages; flat and longer tables pass."""
+    c = Case(zha, [20, 40], 4, 2, 64, 16, BF16, seed=40)
+    q, width = c.queries(2), c.table.shape[1]
+    assert width == 4
+    want, kept = c.run(q), c.table
+    m = {x: ints([0, 0]) for x in ("positions", "slots", "seq_ids")}
+    m["cu"] = ints([0, 0, 0])
+    for bad in (torch.full((2, 5), -1, dtype=torch.int32, device="cuda"), kept.view(4, 2)):
+        c.table = bad
+        with pytest.raises(ValueError, match="table"):
+            c.run(q)
+        with pytest.raises(ValueError, match="table"):
+            zha.paged_plan(c.cfg, bad, c.dlens, ints([0, 0]), ints([0] * c.k.shape[0]), ints([0]), m)
+    for good in (kept.flatten(), torch.cat([kept, kept])):
+        c.table = good
+        assert torch.equal(c.run(q)[0], want[0])

@@ -81,6 +81,12 @@ struct Call {
     int32_t *ints(PyObject *o, const char *name, int64_t n) const {      // None passes
         return o == Py_None ? nullptr : static_cast<int32_t *>(block(o, name, n, at::kInt, false));
     }
+    // [batch, max_pages], or flat: a table of another width would be read askew
+    int32_t *table(PyObject *o, const zha_paged_config *cfg) const {
+        const at::Tensor &t = tensor(o, "table");
+        if (t.dim() > 1 && t.size(-1) != cfg->max_pages) refuse("table", "[batch, " + std::to_string(cfg->max_pages) + "]", t);
+        return ints(o, "table", (int64_t)cfg->batch * cfg->max_pages);
+    }
     void on(const at::Tensor &t) {
         dev = t.get_device();
         if (!t.is_cuda()) refuse("tensors must be on a CUDA device" + shown(t));
@@ -173,7 +179,7 @@ PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int32_t *lens = c.ints(a[2], "lens", B), *n_free = c.ints(a[5], "n_free", 1);
         int32_t *lens_out = a[10] == Py_None ? lens : c.ints(a[10], "lens_out", B);
         int32_t *n_free_out = a[11] == Py_None ? n_free : c.ints(a[11], "n_free_out", 1);
-        int32_t *table = c.ints(a[1], "table", B * cfg->max_pages);
+        int32_t *table = c.table(a[1], cfg);
         const int32_t *n_new = c.ints(a[3], "n_new", B);
         int32_t *free_pages = c.ints(a[4], "free_pages", cfg->n_pages), *status = c.ints(a[12], "dev_status", 1);
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
@@ -230,7 +236,7 @@ PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (ws.get_device() != c.dev || !ws.is_contiguous() || ws.nbytes() < need)
             c.refuse("workspace", "contiguous, on the call's device and of at least " + std::to_string(need) + " bytes", ws);
         const void *k_pool = c.block(a[2], "k_pool", size, type, true), *v_pool = c.block(a[3], "v_pool", size, type, true);
-        const int32_t *table = c.ints(a[4], "table", B * cfg->max_pages), *lens = c.ints(a[5], "lens", B);
+        const int32_t *table = c.table(a[4], cfg), *lens = c.ints(a[5], "lens", B);
         const int32_t *seq = c.ints(a[9], "seq_ids", rows), *pos = c.ints(a[10], "positions", rows);
         int32_t *status = c.ints(a[11], "dev_status", 1);
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
