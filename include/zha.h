@@ -520,6 +520,15 @@ ZHA_API zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary
                                    const int32_t *positions, const int32_t *slots, void *q_out,
                                    void *kpool, void *vpool, int32_t *dev_status, void *stream);
 
+/* What zha_paged_write answers to these arguments before it enqueues anything:
+ * ZHA_OK, or why it refuses them. Nothing is launched or read (host only), so a
+ * caller can ask before zha_paged_plan has moved a step's lengths. */
+ZHA_API zha_status zha_paged_write_check(const zha_paged_config *cfg, const zha_rotary *rotary,
+                                         int32_t n_tokens, const void *q, int64_t q_stride, const void *k_new,
+                                         int64_t k_stride, const void *v_new, int64_t v_stride,
+                                         const int32_t *positions, const int32_t *slots, const void *q_out,
+                                         const void *kpool, const void *vpool);
+
 /* Bytes of scratch zha_paged_decode needs for up to n_rows rows. Zero it once
  * before its first use: every call leaves its counters at zero again. One
  * workspace serves one call at a time (calls that can overlap on the GPU, and

@@ -1,0 +1,60 @@
+"""Calls of the paged cache that are refused or fail, on the GPU: what they leave behind."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def zha():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tree_indexed_sparse_02_b200 import zha as z
+    return z
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def filled_cache(zha, rows=24):
+    """A cache of three sequences after a step of their prompts, and the next step's arguments."""
+    cfg = zha.paged_config(3, 8, 2, 64, 16, 12, 4)
+    cache = zha.PagedCache(cfg, rows, zha.Rotary(64))
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(rows, h, 64, generator=g).to(BF16).cuda() for h in (8, 2, 2))
+    cache.step(ints([9, 4, 8]), q, k, v)
+    torch.cuda.synchronize()
+    cache.check_status()
+    return cache, (ints([1, 1, 1]), q, k, v)
+
+
+def state(cache):
+    return {x: getattr(cache, x).clone() for x in ("table", "lens", "free_pages", "n_free", "k_pool", "v_pool", "out", "lse")}
+
+
+def test_a_refused_step_changes_nothing(zha):
+    cache, (n_new, q, k, v) = filled_cache(zha)
+    before = state(cache)
+    odd = torch.zeros(24 * 8 * 64 + 1, dtype=BF16, device="cuda")[1:].view(24, 8, 64)      # on no 16-byte boundary
+    far = zha.Rotary(64, device="cpu")
+    for args in ((q[:3], k[:3], v[:3]), (q, k, v[:20]), (q.float(), k, v), (q, k, v.transpose(0, 1)), (q, k[:, :1], v),
+                 (q.cpu(), k, v), (odd, k, v)):
+        with pytest.raises((ValueError, zha.ZhaError)):
+            cache.step(n_new, *args)
+    kept = cache.rot
+    for rot in (far, zha.Rotary(128)):                       # on another device; more coordinates than the head has
+        cache.rot = rot
+        with pytest.raises((ValueError, zha.ZhaError)):
+            cache.step(n_new, q, k, v)
+    cache.rot = kept
+    torch.cuda.synchronize()
+    after = state(cache)
+    for x in before:
+        assert torch.equal(before[x], after[x]), x
+    cache.step(n_new, q, k, v)                               # and the step itself still counts its tokens once
+    torch.cuda.synchronize()
+    cache.check_status()
+    assert cache.lens.tolist() == [10, 5, 9]

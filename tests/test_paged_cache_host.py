@@ -1,0 +1,51 @@
+"""PagedCache and the binding's argument handling without a GPU (nothing here launches): a refused call changes nothing."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def zha():
+    from tree_indexed_sparse_02_b200 import build
+    build.build()
+    from tree_indexed_sparse_02_b200 import zha as z
+    return z
+
+
+BASE = dict(batch=3, n_q_heads=8, n_kv_heads=2, head_dim=64, page_size=16, n_pages=10, max_pages=4)
+PTR = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+
+# ---------------------------------------------------------------- a step is refused before anything moves
+
+def test_a_refused_step_enqueues_nothing(zha, monkeypatch):
+    """step() looks at q, k_new and v_new before its first launch (here they are refused for not being on a GPU)."""
+    cache = zha.PagedCache(zha.paged_config(**BASE), 6, device="cpu")
+    launched = []
+    for name in ("paged_plan", "paged_write", "paged_decode"):
+        monkeypatch.setattr(zha, name, lambda *a, _n=name, **kw: launched.append(_n))
+    q, kv = torch.zeros(6, 8, 64, dtype=torch.bfloat16), torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    n_new = torch.ones(3, dtype=torch.int32)
+    for args in ((q, kv, kv), (q[:4], kv[:4], kv[:4]), (q.float(), kv, kv), (q, kv, kv[:, :1])):
+        with pytest.raises(ValueError):
+            cache.step(n_new, *args)
+        assert not launched
+
+
+@pytest.mark.parametrize("at,bad", [(0, None), (1, "desc"), (2, -1), (3, None), (3, ODD), (4, 504), (5, None), (5, ODD), (6, 132), (7, None), (8, -128),
+                                    (9, None), (10, None), (11, ODD), (12, None), (13, ODD)])
+def test_write_check_refuses_what_write_refuses(zha, at, bad):
+    cfg = zha.paged_config(**BASE)
+    rot = zha.RotaryDesc(64, 0, 1.0, 0, 1 << 20)
+    good = [ctypes.byref(cfg), ctypes.byref(rot), 5, PTR, 0, PTR, 0, PTR, 0, PTR, PTR, PTR, PTR, PTR]
+    L = zha.lib()
+    assert L.zha_paged_write_check(*good) == 0
+    if bad == "desc":
+        bad = ctypes.byref(zha.RotaryDesc(128, 0, 1.0, 0, 1 << 20))      # rotates more than the head has
+    args = good[:at] + [bad] + good[at + 1:]
+    assert L.zha_paged_write_check(*args) == L.zha_paged_write(*args, None, None) == 1
+    wide = zha.paged_config(**{**BASE, "n_q_heads": 1032, "n_kv_heads": 129})
+    args = [ctypes.byref(wide)] + good[1:]
+    assert L.zha_paged_write_check(*args) == L.zha_paged_write(*args, None, None) == 2

@@ -23,6 +23,7 @@ namespace {
 decltype(&zha_rotary_apply) f_rotary;
 decltype(&zha_paged_plan) f_plan;
 decltype(&zha_paged_write) f_write;
+decltype(&zha_paged_write_check) f_write_check;
 decltype(&zha_paged_decode) f_decode;
 decltype(&zha_paged_workspace_bytes) f_workspace;
 
@@ -187,9 +188,10 @@ PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// config, rotary, its device, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, status, stream
+// config, rotary, its device, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, status, stream, whether to check
+// the arguments and no more
 PyObject *paged_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 13, [&] {
+    return guarded(n, 14, [&] {
         Call c{"zha_paged_write"};
         const zha_paged_config *cfg = config(a[0]);
         c.on(c.tensor(a[9], "k_pool"));
@@ -210,6 +212,8 @@ PyObject *paged_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *k_pool = c.block(a[9], "k_pool", size, type, true), *v_pool = c.block(a[10], "v_pool", size, type, true);
         int32_t *status = c.ints(a[11], "dev_status", 1);
         const zha_rotary *r = rotation(c, a[1], a[2]);
+        if (a[13] == Py_True)
+            return (int)f_write_check(cfg, r, (int32_t)tokens, qp, qs, kp, ks, vp, vs, pos, slots, qo, k_pool, v_pool);
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
         return (int)f_write(cfg, r, (int32_t)tokens, qp, qs, kp, ks, vp, vs, pos, slots, qo, k_pool, v_pool, status,
                             c.stream(a[12]));
@@ -245,14 +249,16 @@ PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// Addresses of libzha.so's functions: rotary_apply, paged_plan, paged_write, paged_decode, paged_workspace_bytes.
+// Addresses of libzha.so's functions: rotary_apply, paged_plan, paged_write, paged_decode, paged_workspace_bytes,
+// paged_write_check.
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 5, [&] {
+    return guarded(n, 6, [&] {
         f_rotary = reinterpret_cast<decltype(f_rotary)>(PyLong_AsVoidPtr(a[0]));
         f_plan = reinterpret_cast<decltype(f_plan)>(PyLong_AsVoidPtr(a[1]));
         f_write = reinterpret_cast<decltype(f_write)>(PyLong_AsVoidPtr(a[2]));
         f_decode = reinterpret_cast<decltype(f_decode)>(PyLong_AsVoidPtr(a[3]));
         f_workspace = reinterpret_cast<decltype(f_workspace)>(PyLong_AsVoidPtr(a[4]));
+        f_write_check = reinterpret_cast<decltype(f_write_check)>(PyLong_AsVoidPtr(a[5]));
         return 0;
     });
 }

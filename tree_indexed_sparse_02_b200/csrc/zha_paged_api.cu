@@ -54,6 +54,29 @@ bool stride_ok(int64_t *stride, int heads, int d, int es) {
     return *stride >= row && (*stride * es) % 16 == 0 && *stride < (int64_t(1) << 30);
 }
 
+// What a write refuses before it enqueues anything; strides of 0 become the contiguous ones.
+zha_status check_write(const zha_paged_config *cfg, const zha_rotary *rotary, int32_t n_tokens, const void *q,
+                       int64_t *q_stride, const void *k_new, int64_t *k_stride, const void *v_new, int64_t *v_stride,
+                       const int32_t *positions, const int32_t *slots, const void *q_out, const void *kpool,
+                       const void *vpool) {
+    zha_status s = check_paged(cfg);
+    if (s != ZHA_OK) return s;
+    if (rotary && (s = check_rotary(rotary, cfg->head_dim)) != ZHA_OK) return s;
+    if (n_tokens < 0) return ZHA_ERR_INVALID_ARG;
+    if (n_tokens == 0) return ZHA_OK;
+    if (n_tokens > (1 << 30) || cfg->n_q_heads > 1024 || cfg->n_kv_heads > 1024) return ZHA_ERR_UNSUPPORTED;
+    if (!q != !q_out) return ZHA_ERR_INVALID_ARG;
+    if (!k_new || !v_new || !slots || !kpool || !vpool || (rotary && !positions)) return ZHA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(kpool) ||
+        !aligned16(vpool))
+        return ZHA_ERR_INVALID_ARG;
+    const int es = cfg->dtype == ZHA_BF16 ? 2 : 4, d = cfg->head_dim;
+    if ((q && !stride_ok(q_stride, cfg->n_q_heads, d, es)) || !stride_ok(k_stride, cfg->n_kv_heads, d, es) ||
+        !stride_ok(v_stride, cfg->n_kv_heads, d, es))
+        return ZHA_ERR_INVALID_ARG;
+    return ZHA_OK;
+}
+
 zha::PagedAttnArgs attn_args(const zha_paged_config *c, int rows) {
     zha::PagedAttnArgs a{};
     a.rows = rows;
@@ -181,26 +204,23 @@ zha_status zha_rotary_apply(const zha_rotary *rotary, int32_t head_dim, int32_t 
     return cuda_status(zha::launch_rotary(a, static_cast<cudaStream_t>(stream)));
 }
 
+zha_status zha_paged_write_check(const zha_paged_config *cfg, const zha_rotary *rotary, int32_t n_tokens,
+                                 const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
+                                 const void *v_new, int64_t v_stride, const int32_t *positions,
+                                 const int32_t *slots, const void *q_out, const void *kpool, const void *vpool) {
+    return check_write(cfg, rotary, n_tokens, q, &q_stride, k_new, &k_stride, v_new, &v_stride, positions, slots, q_out, kpool,
+                       vpool);
+}
+
 zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary *rotary, int32_t n_tokens,
                            const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
                            const void *v_new, int64_t v_stride, const int32_t *positions,
                            const int32_t *slots, void *q_out, void *kpool, void *vpool,
                            int32_t *dev_status, void *stream) {
-    zha_status s = check_paged(cfg);
-    if (s != ZHA_OK) return s;
-    if (rotary && (s = check_rotary(rotary, cfg->head_dim)) != ZHA_OK) return s;
-    if (n_tokens < 0) return ZHA_ERR_INVALID_ARG;
-    if (n_tokens == 0) return ZHA_OK;
-    if (n_tokens > (1 << 30) || cfg->n_q_heads > 1024 || cfg->n_kv_heads > 1024) return ZHA_ERR_UNSUPPORTED;
-    if (!q != !q_out) return ZHA_ERR_INVALID_ARG;
-    if (!k_new || !v_new || !slots || !kpool || !vpool || (rotary && !positions)) return ZHA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(kpool) ||
-        !aligned16(vpool))
-        return ZHA_ERR_INVALID_ARG;
-    const int es = cfg->dtype == ZHA_BF16 ? 2 : 4, d = cfg->head_dim;
-    if ((q && !stride_ok(&q_stride, cfg->n_q_heads, d, es)) || !stride_ok(&k_stride, cfg->n_kv_heads, d, es) ||
-        !stride_ok(&v_stride, cfg->n_kv_heads, d, es))
-        return ZHA_ERR_INVALID_ARG;
+    const zha_status s = check_write(cfg, rotary, n_tokens, q, &q_stride, k_new, &k_stride, v_new, &v_stride, positions, slots,
+                                     q_out, kpool, vpool);
+    if (s != ZHA_OK || n_tokens == 0) return s;
+    const int d = cfg->head_dim;
     zha::RotaryArgs a{};
     if (rotary) {
         a.freq = rotary->freq;

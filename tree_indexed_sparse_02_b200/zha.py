@@ -125,6 +125,7 @@ def _load():
         "zha_rotary_freqs": ([i32, f64, i32, f64, i64, ctypes.POINTER(f64), ctypes.POINTER(f32)], i32),
         "zha_rotary_apply": ([RP, i32, i32, i32, i32, i32, P, i64, P, i64, P, P, i64, P, i64, i32, P], i32),
         "zha_paged_write": ([PP, RP, i32, P, i64, P, i64, P, i64, P, P, P, P, P, P, P], i32),
+        "zha_paged_write_check": ([PP, RP, i32, P, i64, P, i64, P, i64, P, P, P, P, P], i32),
         "zha_paged_workspace_bytes": ([PP, i32], sz),
         "zha_paged_decode": ([PP, i32, P, P, P, P, P, P, P, P, P, P, P, P], i32),
         "zha_launch_count": ([], ctypes.c_uint64),
@@ -142,7 +143,7 @@ def _load():
 _lib = _load()
 _bind.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
              for name in ("zha_rotary_apply", "zha_paged_plan", "zha_paged_write", "zha_paged_decode",
-                          "zha_paged_workspace_bytes")))
+                          "zha_paged_workspace_bytes", "zha_paged_write_check")))
 
 
 def lib():
@@ -360,10 +361,18 @@ def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out,
     rot None: no rotation; q None: keys and values only."""
     code = _bind.paged_write(ctypes.addressof(cfg), None if rot is None else rot.address, None if rot is None else rot.device, q, k_new,
                              v_new, positions, slots, q_out, k_pool, v_pool, dev_status,
-                             None if stream is None else stream.cuda_stream)
+                             None if stream is None else stream.cuda_stream, False)
     if code:
         raise ZhaError(code, "zha_paged_write")
     return q_out
+
+
+def paged_write_check(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status=None):
+    """Raise what paged_write raises for these arguments; nothing is launched."""
+    code = _bind.paged_write(ctypes.addressof(cfg), None if rot is None else rot.address, None if rot is None else rot.device, q, k_new,
+                             v_new, positions, slots, q_out, k_pool, v_pool, dev_status, None, True)
+    if code:
+        raise ZhaError(code, "zha_paged_write")
 
 
 def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspace, lse=None, seq_ids=None,
@@ -379,7 +388,8 @@ def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspac
 
 class PagedCache:
     """Device state of one layer's paged cache: pools, block table, lengths, free pages, a step's token map and
-    buffers, status. max_tokens is the size of a step's token buffer; shorter steps leave its tail unused.
+    buffers, status. max_tokens is the size of a step's token buffer: q, k_new and v_new always have that many rows,
+    and a step of fewer tokens leaves the last ones unused.
 
     step() runs plan, write and decode; everything stays on the device, so a step can be captured into a CUDA
     graph (n_new, q, k_new, v_new are then the captured buffers). The cache serves one step at a time."""
@@ -423,7 +433,12 @@ class PagedCache:
         return self.out, self.lse
 
     def step(self, n_new, q, k_new, v_new, stream=None):
-        """q [max_tokens, Hq, d], k_new, v_new [max_tokens, Hkv, d]: the step's token rows, before rotation."""
+        """q [max_tokens, Hq, d], k_new, v_new [max_tokens, Hkv, d]: the step's token rows, before rotation.
+
+        A step whose arguments are refused changes nothing: they are checked before the plan moves lengths and pages."""
+        m = self.token_map
+        paged_write_check(self.cfg, self.rot, q, k_new, v_new, m["positions"], m["slots"], self.q, self.k_pool, self.v_pool,
+                          self.status)
         self.plan(n_new, stream)
         self.write(q, k_new, v_new, stream)
         return self.attend(stream)
