@@ -58,3 +58,23 @@ def test_a_refused_step_changes_nothing(zha):
     torch.cuda.synchronize()
     cache.check_status()
     assert cache.lens.tolist() == [10, 5, 9]
+
+
+def test_a_step_without_queries_is_refused(zha):
+    """write() may put keys and values alone; a step would attend with the queries of the step before."""
+    cache, (n_new, q, k, v) = filled_cache(zha)
+    before = state(cache)
+    with pytest.raises(ValueError):
+        cache.step(n_new, None, k, v)
+    torch.cuda.synchronize()
+    after = state(cache)
+    for x in before:
+        assert torch.equal(before[x], after[x]), x
+    cache.plan(n_new)
+    cache.write(None, k, v)
+    torch.cuda.synchronize()
+    cache.check_status()
+    page = int(cache.table[0, 0])
+    want = torch.empty_like(k[:1])
+    zha.rotary(cache.rot, None, k[:1], ints([9]), None, want)
+    assert torch.equal(cache.k_pool[page, :, 9], want[0]) and torch.equal(cache.v_pool[page, :, 9], v[0])

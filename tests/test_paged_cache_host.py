@@ -34,6 +34,18 @@ def test_a_refused_step_enqueues_nothing(zha, monkeypatch):
         assert not launched
 
 
+def test_a_step_without_queries_is_refused(zha, monkeypatch):
+    """With every call of the library let through, a step without queries still is refused, before the first of them."""
+    cache = zha.PagedCache(zha.paged_config(**BASE), 6, device="cpu")
+    launched = []
+    for name in ("paged_write_check", "paged_plan", "paged_write", "paged_decode"):
+        monkeypatch.setattr(zha, name, lambda *a, _n=name, **kw: launched.append(_n))
+    kv = torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q must be"):
+        cache.step(torch.ones(3, dtype=torch.int32), None, kv, kv)
+    assert not launched
+
+
 @pytest.mark.parametrize("at,bad", [(0, None), (1, "desc"), (2, -1), (3, None), (3, ODD), (4, 504), (5, None), (5, ODD), (6, 132), (7, None), (8, -128),
                                     (9, None), (10, None), (11, ODD), (12, None), (13, ODD)])
 def test_write_check_refuses_what_write_refuses(zha, at, bad):

@@ -436,6 +436,8 @@ class PagedCache:
         """q [max_tokens, Hq, d], k_new, v_new [max_tokens, Hkv, d]: the step's token rows, before rotation.
 
         A step whose arguments are refused changes nothing: they are checked before the plan moves lengths and pages."""
+        if q is None:
+            raise ValueError("PagedCache.step: q must be a tensor (write() puts keys and values alone)")
         m = self.token_map
         paged_write_check(self.cfg, self.rot, q, k_new, v_new, m["positions"], m["slots"], self.q, self.k_pool, self.v_pool,
                           self.status)
