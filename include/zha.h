@@ -533,7 +533,8 @@ ZHA_API zha_status zha_paged_write_check(const zha_paged_config *cfg, const zha_
  * before its first use: every call leaves its counters at zero again. One
  * workspace serves one call at a time (calls that can overlap on the GPU, and
  * graphs that can, need one each); calls of different configurations may share
- * one that is large enough for each. 0 for a bad config or n_rows < 1. */
+ * one that is large enough for each. 0 for a bad config, n_rows < 1, or more
+ * rows than zha_paged_decode takes of this configuration. */
 ZHA_API size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_rows);
 
 /*

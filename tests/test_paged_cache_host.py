@@ -61,3 +61,35 @@ def test_write_check_refuses_what_write_refuses(zha, at, bad):
     wide = zha.paged_config(**{**BASE, "n_q_heads": 1032, "n_kv_heads": 129})
     args = [ctypes.byref(wide)] + good[1:]
     assert L.zha_paged_write_check(*args) == L.zha_paged_write(*args, None, None) == 2
+
+
+# ---------------------------------------------------------------- limits that every step would meet
+
+def test_a_cache_that_no_step_could_use_is_refused(zha):
+    """Rows and tables beyond zha_paged_decode's limits, heads beyond zha_paged_write's, a rotation of more than a head."""
+    L = zha.lib()
+    big = zha.paged_config(4, 16, 8, 64, page_size=64, n_pages=1, max_pages=8193)         # 16,384 x 8 x 524,352 > 2^35
+    args = [ctypes.byref(big), 16384, PTR, PTR, PTR, PTR, PTR, PTR, None, PTR, None, PTR, None, None]
+    assert L.zha_paged_decode(*args) == 2
+    assert zha.paged_workspace_bytes(big, 16384) == 0
+    wide = zha.paged_config(4, 2048, 128, 64, page_size=1, n_pages=1, max_pages=1)
+    for cfg, rows, rot in ((big, 16384, None), (wide, 1, None), (zha.paged_config(**BASE), 1 << 22, None)):
+        with pytest.raises(zha.ZhaError) as e:
+            zha.PagedCache(cfg, rows, rot, device="cpu")
+        assert e.value.code == 2
+    with pytest.raises(zha.ZhaError) as e:
+        zha.PagedCache(zha.paged_config(**BASE), 4, zha.Rotary(128, device="cpu"), device="cpu")
+    assert e.value.code == 1
+    for rows in (0, -1):
+        with pytest.raises(zha.ZhaError) as e:
+            zha.PagedCache(zha.paged_config(**BASE), rows, device="cpu")
+        assert e.value.code == 1
+
+
+@pytest.mark.parametrize("hq,hkv,page,width,most", [(2, 2, 1024, 1 << 14, 1024), (16, 1, 1, 1, 1 << 20), (5, 5, 64, 4096, 26214)])
+def test_workspace_and_decode_draw_one_line(zha, hq, hkv, page, width, most):
+    cfg = zha.paged_config(1, hq, hkv, 64, page, 1, width)
+    assert zha.paged_workspace_bytes(cfg, most) > 0 and zha.paged_workspace_bytes(cfg, most + 1) == 0
+    args = lambda n, ws: [ctypes.byref(cfg), n, PTR, PTR, PTR, PTR, PTR, PTR, None, PTR, None, ws, None, None]  # noqa: E731
+    assert zha.lib().zha_paged_decode(*args(most + 1, PTR)) == 2
+    assert zha.lib().zha_paged_decode(*args(most, None)) == 1             # as far as the missing workspace

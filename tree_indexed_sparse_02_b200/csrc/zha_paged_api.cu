@@ -39,6 +39,12 @@ zha_status check_paged(const zha_paged_config *c) {
     return ZHA_OK;
 }
 
+// Rows of one attention call: counts of query heads and of tiles (of 32 tokens at least) stay in int32.
+bool rows_ok(const zha_paged_config *c, int32_t n_rows) {
+    return (int64_t)n_rows * c->n_q_heads <= (1 << 24) &&
+           (int64_t)n_rows * c->n_kv_heads <= (int64_t(1) << 35) / c->page_size / c->max_pages;
+}
+
 zha_status check_rotary(const zha_rotary *r, int head_dim) {
     if (r->rotary_dim < 2 || (r->rotary_dim & 1) || r->rotary_dim > head_dim || r->reserved) return ZHA_ERR_INVALID_ARG;
     if (r->layout != ZHA_ROPE_HALF && r->layout != ZHA_ROPE_INTERLEAVED) return ZHA_ERR_INVALID_ARG;
@@ -253,7 +259,7 @@ zha_status zha_paged_write(const zha_paged_config *cfg, const zha_rotary *rotary
 }
 
 size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_rows) {
-    if (check_paged(cfg) != ZHA_OK || n_rows < 1) return 0;
+    if (check_paged(cfg) != ZHA_OK || n_rows < 1 || !rows_ok(cfg, n_rows)) return 0;
     return zha::paged_attn_workspace(attn_args(cfg, n_rows));
 }
 
@@ -265,9 +271,7 @@ zha_status zha_paged_decode(const zha_paged_config *cfg, int32_t n_rows, const v
     if (s != ZHA_OK) return s;
     if (n_rows < 0 || (!seq_ids && n_rows > cfg->batch)) return ZHA_ERR_INVALID_ARG;
     if (n_rows == 0) return ZHA_OK;
-    // counts of query heads and of tiles (of 32 tokens at least) in int32
-    if ((int64_t)n_rows * cfg->n_q_heads > (1 << 24)) return ZHA_ERR_UNSUPPORTED;
-    if ((int64_t)n_rows * cfg->n_kv_heads > (int64_t(1) << 35) / cfg->page_size / cfg->max_pages) return ZHA_ERR_UNSUPPORTED;
+    if (!rows_ok(cfg, n_rows)) return ZHA_ERR_UNSUPPORTED;
     if (!q || !kpool || !vpool || !table || !lens || !out || !workspace) return ZHA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) || !aligned16(workspace))
         return ZHA_ERR_INVALID_ARG;

@@ -296,7 +296,8 @@ def paged_workspace(cfg: PagedConfig, rows: int, device="cuda"):
     """Zeroed scratch of paged_decode calls of up to `rows` rows (one call at a time)."""
     n = paged_workspace_bytes(cfg, rows)
     if n == 0:
-        raise ZhaError(1, "zha_paged_workspace_bytes")
+        check(_lib.zha_paged_check_config(ctypes.byref(cfg)), "zha_paged_check_config")
+        raise ZhaError(1 if rows < 1 else 2, "zha_paged_workspace_bytes")
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
@@ -397,6 +398,10 @@ class PagedCache:
     def __init__(self, cfg: PagedConfig, max_tokens: int, rot: Rotary | None = None, device="cuda"):
         self.cfg, self.rot = cfg, rot
         kw = dict(dtype=torch.int32, device=device)
+        # what no step's attention or write would take is refused here (16: an address that the check does not read)
+        self.workspace = paged_workspace(cfg, max_tokens, device)
+        check(_lib.zha_paged_write_check(ctypes.byref(cfg), None if rot is None else ctypes.byref(rot.desc), max_tokens,
+                                         *[16, 0] * 3, *[16] * 5), "zha_paged_write")
         shape = (cfg.n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
         self.k_pool = torch.zeros(shape, dtype=cfg.torch_dtype, device=device)
         self.v_pool = torch.zeros(shape, dtype=cfg.torch_dtype, device=device)
@@ -410,7 +415,6 @@ class PagedCache:
         self.q = torch.zeros(rows, dtype=cfg.torch_dtype, device=device)
         self.out = torch.zeros(rows, dtype=cfg.torch_dtype, device=device)
         self.lse = torch.zeros(rows[:2], dtype=torch.float32, device=device)
-        self.workspace = paged_workspace(cfg, max_tokens, device)
         self.status = torch.zeros(1, **kw)
 
     def plan(self, n_new, stream=None):
