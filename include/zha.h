@@ -556,7 +556,8 @@ ZHA_API size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_
  * row's parts are joined in a fixed order). A row whose every score is -inf
  * gets zeros and -inf as well. Every wait inside is bounded (about two
  * seconds): ZHA_ERR_TIMEOUT, the results are then invalid and the workspace is
- * to be zeroed again. n_rows * n_q_heads <= 2^24 and
+ * to be zeroed again (after any device error, where dev_status is shared: the
+ * first one is kept, and hides a later ZHA_ERR_TIMEOUT). n_rows * n_q_heads <= 2^24 and
  * n_rows * n_kv_heads * max_pages * page_size <= 2^35, otherwise
  * ZHA_ERR_UNSUPPORTED.
  */

@@ -19,13 +19,14 @@ def ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def filled_cache(zha, rows=24):
+def filled_cache(zha, rows=24, prompts=(9, 4, 8)):
     """A cache of three sequences after a step of their prompts, and the next step's arguments."""
-    cfg = zha.paged_config(3, 8, 2, 64, 16, 12, 4)
+    width = (max(prompts) + 64) // 16
+    cfg = zha.paged_config(3, 8, 2, 64, 16, 3 * width, width)
     cache = zha.PagedCache(cfg, rows, zha.Rotary(64))
     g = torch.Generator().manual_seed(1)
     q, k, v = (torch.randn(rows, h, 64, generator=g).to(BF16).cuda() for h in (8, 2, 2))
-    cache.step(ints([9, 4, 8]), q, k, v)
+    cache.step(ints(prompts), q, k, v)
     torch.cuda.synchronize()
     cache.check_status()
     return cache, (ints([1, 1, 1]), q, k, v)
@@ -78,3 +79,34 @@ def test_a_step_without_queries_is_refused(zha):
     want = torch.empty_like(k[:1])
     zha.rotary(cache.rot, None, k[:1], ints([9]), None, want)
     assert torch.equal(cache.k_pool[page, :, 9], want[0]) and torch.equal(cache.v_pool[page, :, 9], v[0])
+
+
+def test_steps_after_a_wait_ran_out(zha):
+    """What a call leaves that gave up, written from the host: the step after check_status is right again, on another
+    stream too, and as a replay of a graph captured before."""
+    for stream, captured in ((None, False), (torch.cuda.Stream(), False), (None, True)):
+        prompts = (4000, 300, 8)                             # rows long enough to be split over several CTAs
+        cache, (n_new, q, k, v) = filled_cache(zha, 4320, prompts)
+        same, _ = filled_cache(zha, 4320, prompts)
+        assert torch.equal(cache.out, same.out)
+        if captured:
+            none = torch.zeros_like(n_new)
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                cache.step(none, q, k, v)
+            none.copy_(n_new)
+        cache.workspace.view(torch.int32)[:1776] = 2         # every counter
+        cache.status.fill_(5)
+        with pytest.raises(zha.ZhaError) as e:
+            cache.check_status()
+        assert e.value.code == 5
+        if captured:
+            graph.replay()
+        else:
+            cache.step(n_new, q, k, v, stream)
+        want, lse = same.step(n_new, q, k, v)
+        torch.cuda.synchronize()
+        cache.check_status()
+        assert torch.equal(cache.out[:3], want[:3]) and torch.equal(cache.lse[:3], lse[:3])
+        assert cache.lens.tolist() == [4001, 301, 9]

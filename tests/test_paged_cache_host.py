@@ -93,3 +93,19 @@ def test_workspace_and_decode_draw_one_line(zha, hq, hkv, page, width, most):
     args = lambda n, ws: [ctypes.byref(cfg), n, PTR, PTR, PTR, PTR, PTR, PTR, None, PTR, None, ws, None, None]  # noqa: E731
     assert zha.lib().zha_paged_decode(*args(most + 1, PTR)) == 2
     assert zha.lib().zha_paged_decode(*args(most, None)) == 1             # as far as the missing workspace
+
+
+# ---------------------------------------------------------------- errors on the device
+
+@pytest.mark.parametrize("code", [5, 3, 1])
+def test_an_error_clears_the_workspace(zha, code):
+    """A wait that ran out leaves counters behind; the status may show an earlier error instead of it."""
+    cache = zha.PagedCache(zha.paged_config(**BASE), 6, device="cpu")
+    cache.workspace.view(torch.int32)[[0, 7, 500]] = 3
+    cache.check_status()                                     # no error: nothing is touched
+    assert cache.workspace.any()
+    cache.status.fill_(code)
+    with pytest.raises(zha.ZhaError) as e:
+        cache.check_status("step")
+    assert e.value.code == code
+    assert not cache.workspace.any() and not cache.status.any()

@@ -450,9 +450,17 @@ class PagedCache:
         return self.attend(stream)
 
     def check_status(self, where="device"):
+        """Raise what steps of the current stream have set since the last look. The workspace is cleared then: a call
+        that gave up on a wait leaves counters in it, and a status that was set before hides that."""
         code = int(self.status.item())
         if code:
+            on_gpu = self.status.is_cuda
+            if on_gpu:
+                torch.cuda.synchronize(self.status.device)
             self.status.zero_()
+            self.workspace.zero_()
+            if on_gpu:                                       # before a step on any stream
+                torch.cuda.synchronize(self.status.device)
             raise ZhaError(code, where)
 
 
