@@ -109,3 +109,32 @@ def test_an_error_clears_the_workspace(zha, code):
         cache.check_status("step")
     assert e.value.code == code
     assert not cache.workspace.any() and not cache.status.any()
+
+
+# ---------------------------------------------------------------- configurations and rotations of another type
+
+def test_structures_of_another_type_are_refused(zha):
+    """The calls take a structure's address: any other one would be read field by field as a paged configuration."""
+    import types
+    cfg, rot = zha.paged_config(**BASE), zha.Rotary(64, device="cpu")
+    other = zha.config(3, 8, 2, 64, 16, 2, 1)
+    q, kv = torch.zeros(3, 8, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    pool, i32 = torch.zeros(10, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(12, dtype=torch.int32)
+    m = {"positions": i32, "slots": i32, "seq_ids": i32, "cu": i32}
+    for bad in (other, rot.desc, ctypes.c_int32(3), 1 << 20, None, ctypes.byref(cfg), "cfg"):
+        with pytest.raises(TypeError, match="PagedConfig"):
+            zha.paged_plan(bad, i32, i32, i32, i32, i32, m)
+        for call in (zha.paged_write, zha.paged_write_check):
+            with pytest.raises(TypeError, match="PagedConfig"):
+                call(bad, rot, q, kv, kv, i32, i32, q, pool, pool)
+        with pytest.raises(TypeError, match="PagedConfig"):
+            zha.paged_decode(bad, q, pool, pool, i32, i32, q, i32)
+    like = types.SimpleNamespace(address=ctypes.addressof(cfg), device=-1, desc=cfg)
+    for bad in (cfg, rot.desc, like, 64):
+        with pytest.raises(TypeError, match="Rotary"):
+            zha.rotary(bad, q, kv, i32)
+        for call in (zha.paged_write, zha.paged_write_check):
+            with pytest.raises(TypeError, match="Rotary"):
+                call(cfg, bad, q, kv, kv, i32, i32, q, pool, pool)
+    with pytest.raises(TypeError, match="Rotary"):
+        zha.rotary(None, q, kv, i32)
