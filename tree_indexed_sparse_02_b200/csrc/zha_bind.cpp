@@ -27,9 +27,16 @@ decltype(&zha_paged_write_check) f_write_check;
 decltype(&zha_paged_decode) f_decode;
 decltype(&zha_paged_workspace_bytes) f_workspace;
 
+PyTypeObject *paged_config_type, *rotary_type;       // zha.PagedConfig and zha.Rotary
+PyObject *name_desc, *name_device;
+
 struct Refused : std::runtime_error {
     using std::runtime_error::runtime_error;
 };
+struct WrongType : std::runtime_error {
+    using std::runtime_error::runtime_error;
+};
+struct Raised {};                        // a Python error is set
 
 std::string list(at::IntArrayRef v) {
     std::string s = "[";
@@ -102,13 +109,46 @@ at::ScalarType type_of(const zha_paged_config *c) { return c->dtype == ZHA_BF16 
 int64_t pool_elements(const zha_paged_config *c) {
     return (int64_t)c->n_pages * c->n_kv_heads * c->page_size * c->head_dim;
 }
-const zha_paged_config *config(PyObject *o) { return static_cast<const zha_paged_config *>(PyLong_AsVoidPtr(o)); }
 
-// The rotation's description (an address, or None) and the device its table is on.
-const zha_rotary *rotation(const Call &c, PyObject *o, PyObject *device) {
+// The memory of a ctypes structure (which its owner keeps). Only of the right type: any other one would be read askew.
+template <typename S>
+const S *memory(PyObject *o) {
+    Py_buffer b;
+    if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE)) throw Raised();
+    const S *p = b.len >= (Py_ssize_t)sizeof(S) ? static_cast<const S *>(b.buf) : nullptr;
+    PyBuffer_Release(&b);
+    if (!p) throw WrongType("a structure is too small");
+    return p;
+}
+const zha_paged_config *config(PyObject *o) {
+    if (!PyObject_TypeCheck(o, paged_config_type)) throw WrongType(std::string("a PagedConfig is needed, got ") + Py_TYPE(o)->tp_name);
+    return memory<zha_paged_config>(o);
+}
+
+void is_rotary(PyObject *o) {
+    if (!PyObject_TypeCheck(o, rotary_type)) throw WrongType(std::string("a Rotary is needed, got ") + Py_TYPE(o)->tp_name);
+}
+// The description of a rotation whose table is on the call's device; null for None.
+const zha_rotary *rotation(const Call &c, PyObject *o) {
     if (o == Py_None) return nullptr;
-    if (PyLong_AsLong(device) != c.dev) c.refuse("the rotary table is on another device than the tensors");
-    return static_cast<const zha_rotary *>(PyLong_AsVoidPtr(o));
+    PyObject *device = PyObject_GetAttr(o, name_device), *desc = PyObject_GetAttr(o, name_desc);
+    const zha_rotary *r = nullptr;
+    long dev = -1;
+    if (device && desc) {
+        dev = PyLong_AsLong(device);
+        try {
+            r = memory<zha_rotary>(desc);
+        } catch (...) {
+            Py_DECREF(device);
+            Py_DECREF(desc);               // (the rotation holds it)
+            throw;
+        }
+    }
+    Py_XDECREF(device);
+    Py_XDECREF(desc);
+    if (!r || PyErr_Occurred()) throw Raised();
+    if (dev != c.dev) c.refuse("the rotary table is on another device than the tensors");
+    return r;
 }
 
 template <typename F>
@@ -120,6 +160,9 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
     try {
         const int code = f();
         return PyErr_Occurred() ? nullptr : PyLong_FromLong(code);
+    } catch (const Raised &) {
+    } catch (const WrongType &e) {
+        PyErr_SetString(PyExc_TypeError, e.what());
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const std::exception &e) {
@@ -130,13 +173,14 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
     return nullptr;
 }
 
-// rotary, its device, q, k, positions, q_out, k_out, transpose, stream
+// rotary, q, k, positions, q_out, k_out, transpose, stream
 PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 9, [&] {
+    return guarded(n, 8, [&] {
         Call c{"zha_rotary_apply"};
-        const bool has_q = a[2] != Py_None, has_k = a[3] != Py_None;
+        is_rotary(a[0]);
+        const bool has_q = a[1] != Py_None, has_k = a[2] != Py_None;
         if (!has_q && !has_k) c.refuse("q or k [n, heads, d] is needed");
-        const at::Tensor &one = c.tensor(has_q ? a[2] : a[3], has_q ? "q" : "k");
+        const at::Tensor &one = c.tensor(has_q ? a[1] : a[2], has_q ? "q" : "k");
         if (one.dim() != 3) c.refuse(has_q ? "q" : "k", "[n, heads, d]", one);
         c.on(one);
         const auto type = one.scalar_type();
@@ -146,20 +190,20 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int64_t hk = 0, qs = 0, qos = 0, ks = 0, kos = 0;
         void *qp = nullptr, *qo = nullptr, *kp = nullptr, *ko = nullptr;
         if (has_q) {
-            qp = c.rows(a[2], "q", tokens, hq, d, type, qs);
-            qo = a[5] == Py_None ? (qos = qs, qp) : c.rows(a[5], "q_out", tokens, hq, d, type, qos);
+            qp = c.rows(a[1], "q", tokens, hq, d, type, qs);
+            qo = a[4] == Py_None ? (qos = qs, qp) : c.rows(a[4], "q_out", tokens, hq, d, type, qos);
         }
         if (has_k) {
-            const at::Tensor &k = c.tensor(a[3], "k");
+            const at::Tensor &k = c.tensor(a[2], "k");
             hk = k.dim() == 3 ? k.size(1) : 0;
-            kp = c.rows(a[3], "k", tokens, hk, d, type, ks);
-            ko = a[6] == Py_None ? (kos = ks, kp) : c.rows(a[6], "k_out", tokens, hk, d, type, kos);
+            kp = c.rows(a[2], "k", tokens, hk, d, type, ks);
+            ko = a[5] == Py_None ? (kos = ks, kp) : c.rows(a[5], "k_out", tokens, hk, d, type, kos);
         }
-        const int32_t *pos = c.ints(a[4], "positions", tokens);
-        const zha_rotary *r = rotation(c, a[0], a[1]);
+        const int32_t *pos = c.ints(a[3], "positions", tokens);
+        const zha_rotary *r = rotation(c, a[0]);
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
         return (int)f_rotary(r, (int32_t)d, type == at::kFloat ? ZHA_F32 : ZHA_BF16, (int32_t)tokens, (int32_t)hq, (int32_t)hk,
-                             qp, qs, kp, ks, pos, qo, qos, ko, kos, PyObject_IsTrue(a[7]) == 1, c.stream(a[8]));
+                             qp, qs, kp, ks, pos, qo, qos, ko, kos, PyObject_IsTrue(a[6]) == 1, c.stream(a[7]));
     });
 }
 
@@ -188,35 +232,36 @@ PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// config, rotary, its device, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, status, stream, whether to check
+// config, rotary, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, status, stream, whether to check
 // the arguments and no more
 PyObject *paged_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 14, [&] {
+    return guarded(n, 13, [&] {
         Call c{"zha_paged_write"};
         const zha_paged_config *cfg = config(a[0]);
-        c.on(c.tensor(a[9], "k_pool"));
+        if (a[1] != Py_None) is_rotary(a[1]);
+        c.on(c.tensor(a[8], "k_pool"));
         const auto type = type_of(cfg);
         const int64_t d = cfg->head_dim, hkv = cfg->n_kv_heads, hq = cfg->n_q_heads, size = pool_elements(cfg);
-        const at::Tensor &k = c.tensor(a[4], "k_new");
+        const at::Tensor &k = c.tensor(a[3], "k_new");
         const int64_t tokens = k.dim() ? k.size(0) : 0;
         if (tokens > INT32_MAX) c.refuse("too many tokens");
         int64_t qs = 0, ks = 0, vs = 0;
-        const void *kp = c.rows(a[4], "k_new", tokens, hkv, d, type, ks), *vp = c.rows(a[5], "v_new", tokens, hkv, d, type, vs);
+        const void *kp = c.rows(a[3], "k_new", tokens, hkv, d, type, ks), *vp = c.rows(a[4], "v_new", tokens, hkv, d, type, vs);
         void *qp = nullptr, *qo = nullptr;
-        if (a[3] != Py_None) {
-            qp = c.rows(a[3], "q", tokens, hq, d, type, qs);
-            if (a[8] == Py_None) c.refuse("q_out is needed with q");
-            qo = c.block(a[8], "q_out", tokens * hq * d, type, true);
+        if (a[2] != Py_None) {
+            qp = c.rows(a[2], "q", tokens, hq, d, type, qs);
+            if (a[7] == Py_None) c.refuse("q_out is needed with q");
+            qo = c.block(a[7], "q_out", tokens * hq * d, type, true);
         }
-        const int32_t *pos = c.ints(a[6], "positions", tokens), *slots = c.ints(a[7], "slots", tokens);
-        void *k_pool = c.block(a[9], "k_pool", size, type, true), *v_pool = c.block(a[10], "v_pool", size, type, true);
-        int32_t *status = c.ints(a[11], "dev_status", 1);
-        const zha_rotary *r = rotation(c, a[1], a[2]);
-        if (a[13] == Py_True)
+        const int32_t *pos = c.ints(a[5], "positions", tokens), *slots = c.ints(a[6], "slots", tokens);
+        void *k_pool = c.block(a[8], "k_pool", size, type, true), *v_pool = c.block(a[9], "v_pool", size, type, true);
+        int32_t *status = c.ints(a[10], "dev_status", 1);
+        const zha_rotary *r = rotation(c, a[1]);
+        if (a[12] == Py_True)
             return (int)f_write_check(cfg, r, (int32_t)tokens, qp, qs, kp, ks, vp, vs, pos, slots, qo, k_pool, v_pool);
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
         return (int)f_write(cfg, r, (int32_t)tokens, qp, qs, kp, ks, vp, vs, pos, slots, qo, k_pool, v_pool, status,
-                            c.stream(a[12]));
+                            c.stream(a[11]));
     });
 }
 
@@ -250,15 +295,22 @@ PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // Addresses of libzha.so's functions: rotary_apply, paged_plan, paged_write, paged_decode, paged_workspace_bytes,
-// paged_write_check.
+// paged_write_check; then the types PagedConfig and Rotary.
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 6, [&] {
+    return guarded(n, 8, [&] {
         f_rotary = reinterpret_cast<decltype(f_rotary)>(PyLong_AsVoidPtr(a[0]));
         f_plan = reinterpret_cast<decltype(f_plan)>(PyLong_AsVoidPtr(a[1]));
         f_write = reinterpret_cast<decltype(f_write)>(PyLong_AsVoidPtr(a[2]));
         f_decode = reinterpret_cast<decltype(f_decode)>(PyLong_AsVoidPtr(a[3]));
         f_workspace = reinterpret_cast<decltype(f_workspace)>(PyLong_AsVoidPtr(a[4]));
         f_write_check = reinterpret_cast<decltype(f_write_check)>(PyLong_AsVoidPtr(a[5]));
+        if (!PyType_Check(a[6]) || !PyType_Check(a[7])) throw WrongType("types are needed");
+        Py_INCREF(a[6]);
+        Py_INCREF(a[7]);
+        paged_config_type = reinterpret_cast<PyTypeObject *>(a[6]);
+        rotary_type = reinterpret_cast<PyTypeObject *>(a[7]);
+        name_desc = PyUnicode_InternFromString("desc");
+        name_device = PyUnicode_InternFromString("device");
         return 0;
     });
 }

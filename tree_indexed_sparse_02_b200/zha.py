@@ -141,9 +141,6 @@ def _load():
 
 
 _lib = _load()
-_bind.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
-             for name in ("zha_rotary_apply", "zha_paged_plan", "zha_paged_write", "zha_paged_decode",
-                          "zha_paged_workspace_bytes", "zha_paged_write_check")))
 
 
 def lib():
@@ -331,31 +328,18 @@ class Rotary:
         return twin
 
 
-# The calls below check their tensors (type, shape, layout, device: ValueError) and pass them on in csrc/zha_bind.cpp:
-# on the GPU they can take less time than Python takes to look at the tensors' attributes. Configurations and
-# rotations go there as addresses, so their types are looked at here.
-
-def _paged(cfg):
-    if not isinstance(cfg, PagedConfig):
-        raise TypeError(f"a PagedConfig is needed, got {type(cfg).__name__}")
-    return ctypes.addressof(cfg)
-
-
-def _turn(rot):
-    """Address of a rotation's description and the device of its table."""
-    if rot is None:
-        return None, None
-    if not isinstance(rot, Rotary):
-        raise TypeError(f"a Rotary is needed, got {type(rot).__name__}")
-    return rot.address, rot.device
+# The calls below check their arguments (tensors' type, shape, layout, device: ValueError; PagedConfig and Rotary:
+# TypeError) and pass them on in csrc/zha_bind.cpp: on the GPU they can take less time than Python takes to look at
+# the tensors' attributes.
+_bind.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
+             for name in ("zha_rotary_apply", "zha_paged_plan", "zha_paged_write", "zha_paged_decode",
+                          "zha_paged_workspace_bytes", "zha_paged_write_check")), PagedConfig, Rotary)
 
 
 def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
     """Rotate q [n, Hq, d] and k [n, Hk, d] (either may be None; tokens may be strided) at int32 positions [n].
     The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out)."""
-    if rot is None:
-        raise TypeError("a Rotary is needed, got None")
-    code = _bind.rotary(*_turn(rot), q, k, positions, q_out, k_out, transpose,
+    code = _bind.rotary(rot, q, k, positions, q_out, k_out, transpose,
                         None if stream is None else stream.cuda_stream)
     if code:
         raise ZhaError(code, "zha_rotary_apply")
@@ -368,7 +352,7 @@ def paged_plan(cfg: PagedConfig, table, lens, n_new, free_pages, n_free, token_m
     token_map: {"positions", "slots", "seq_ids"} (one entry per row of the token buffer) and "cu" [batch + 1];
     lens_out and n_free_out default to lens and n_free (in place)."""
     m = token_map
-    code = _bind.paged_plan(_paged(cfg), table, lens, n_new, free_pages, n_free, m["positions"], m["slots"], m["seq_ids"],
+    code = _bind.paged_plan(cfg, table, lens, n_new, free_pages, n_free, m["positions"], m["slots"], m["seq_ids"],
                             m["cu"], lens_out, n_free_out, dev_status, None if stream is None else stream.cuda_stream)
     if code:
         raise ZhaError(code, "zha_paged_plan")
@@ -378,7 +362,7 @@ def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out,
                 stream=None):
     """Rotate q and k_new [n, heads, d] and write k_new, v_new to their cache slots [n] (negative: skipped).
     rot None: no rotation; q None: keys and values only."""
-    code = _bind.paged_write(_paged(cfg), *_turn(rot), q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status,
+    code = _bind.paged_write(cfg, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status,
                              None if stream is None else stream.cuda_stream, False)
     if code:
         raise ZhaError(code, "zha_paged_write")
@@ -387,7 +371,7 @@ def paged_write(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out,
 
 def paged_write_check(cfg: PagedConfig, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status=None):
     """Raise what paged_write raises for these arguments; nothing is launched."""
-    code = _bind.paged_write(_paged(cfg), *_turn(rot), q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status, None, True)
+    code = _bind.paged_write(cfg, rot, q, k_new, v_new, positions, slots, q_out, k_pool, v_pool, dev_status, None, True)
     if code:
         raise ZhaError(code, "zha_paged_write")
 
@@ -396,7 +380,7 @@ def paged_decode(cfg: PagedConfig, q, k_pool, v_pool, table, lens, out, workspac
                  positions=None, dev_status=None, stream=None):
     """Attention of rows q [n, Hq, d] over the paged cache into out (and lse [n, Hq] fp32). Row r is of sequence
     seq_ids[r] (default r; negative: left as it is) and attends tokens 0 .. positions[r] (default: all)."""
-    code = _bind.paged_decode(_paged(cfg), q, k_pool, v_pool, table, lens, out, workspace, lse, seq_ids, positions,
+    code = _bind.paged_decode(cfg, q, k_pool, v_pool, table, lens, out, workspace, lse, seq_ids, positions,
                               dev_status, None if stream is None else stream.cuda_stream)
     if code:
         raise ZhaError(code, "zha_paged_decode")
