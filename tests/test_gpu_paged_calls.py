@@ -110,3 +110,25 @@ def test_steps_after_a_wait_ran_out(zha):
         cache.check_status()
         assert torch.equal(cache.out[:3], want[:3]) and torch.equal(cache.lse[:3], lse[:3])
         assert cache.lens.tolist() == [4001, 301, 9]
+
+
+def test_arguments_that_raise_enqueue_nothing(zha):
+    """A transpose flag without a truth value, a stream whose handle is no number: the error, and nothing written."""
+    class Stream:
+        cuda_stream = "17"
+
+    x = torch.randn(5, 2, 64, generator=torch.Generator().manual_seed(2)).cuda()
+    pos, kept = ints([1, 2, 3, 4, 5]), x.clone()
+    rot = zha.Rotary(64)
+    before = zha.launch_count()
+    for kw in (dict(transpose=torch.ones(2)), dict(stream=Stream())):
+        with pytest.raises((RuntimeError, TypeError)):
+            zha.rotary(rot, x, None, pos, **kw)
+    cfg = zha.paged_config(1, 2, 2, 64, 16, 1, 1, dtype="f32")
+    pool = torch.zeros(1, 2, 16, 64, device="cuda")
+    with pytest.raises(TypeError):
+        zha.paged_write(cfg, None, None, x, x, None, pos, None, pool, pool.clone(), stream=Stream())
+    with pytest.raises(TypeError):
+        zha.paged_decode(cfg, x[:1], pool, pool, ints([0]), ints([3]), x[1:2], zha.paged_workspace(cfg, 1), stream=Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(x, kept) and not pool.any() and zha.launch_count() == before

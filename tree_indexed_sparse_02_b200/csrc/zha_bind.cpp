@@ -100,7 +100,11 @@ struct Call {
         if (!t.is_cuda()) refuse("tensors must be on a CUDA device" + shown(t));
     }
     void *stream(PyObject *o) const {
-        if (o != Py_None) return PyLong_AsVoidPtr(o);
+        if (o != Py_None) {
+            void *st = PyLong_AsVoidPtr(o);
+            if (!st && PyErr_Occurred()) throw Raised();       // not the default stream in its place
+            return st;
+        }
         return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
     }
 };
@@ -201,9 +205,11 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const int32_t *pos = c.ints(a[3], "positions", tokens);
         const zha_rotary *r = rotation(c, a[0]);
+        const int transpose = PyObject_IsTrue(a[6]);
+        if (transpose < 0) throw Raised();
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
         return (int)f_rotary(r, (int32_t)d, type == at::kFloat ? ZHA_F32 : ZHA_BF16, (int32_t)tokens, (int32_t)hq, (int32_t)hk,
-                             qp, qs, kp, ks, pos, qo, qos, ko, kos, PyObject_IsTrue(a[6]) == 1, c.stream(a[7]));
+                             qp, qs, kp, ks, pos, qo, qos, ko, kos, transpose, c.stream(a[7]));
     });
 }
 
