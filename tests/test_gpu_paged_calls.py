@@ -132,3 +132,49 @@ def test_arguments_that_raise_enqueue_nothing(zha):
         zha.paged_decode(cfg, x[:1], pool, pool, ints([0]), ints([3]), x[1:2], zha.paged_workspace(cfg, 1), stream=Stream())
     torch.cuda.synchronize()
     assert torch.equal(x, kept) and not pool.any() and zha.launch_count() == before
+
+
+def test_arrays_of_another_layout_are_refused(zha):
+    """Pools, outputs and lse of the right number of elements in another order (tokens before heads, pages of another
+    size, heads before rows) were read and written askew; shapes that only merge neighbours mean the same array."""
+    n, hq, hkv, d, page, pages = 3, 8, 4, 64, 16, 6
+    cfg = zha.paged_config(n, hq, hkv, d, page, pages, 2)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(pages, hkv, page, d, generator=g).to(BF16).cuda() for _ in range(2))
+    q = torch.randn(n, hq, d, generator=g).to(BF16).cuda()
+    kv = torch.randn(n, hkv, d, generator=g).to(BF16).cuda()
+    table, lens, slots = ints([[0, 1], [2, 3], [4, 5]]), ints([20, 7, 32]), ints([3, 50, 90])
+    ws = zha.paged_workspace(cfg, n)
+
+    def decode(k=k, v=v, out=None, lse=None):
+        out = torch.zeros(n, hq, d, dtype=BF16, device="cuda") if out is None else out
+        zha.paged_decode(cfg, q, k, v, table, lens, out, ws, lse=lse)
+        return out
+
+    def write(k=k, v=v, q_out=None):
+        zha.paged_write(cfg, None, q, kv, kv, None, slots, torch.empty_like(q) if q_out is None else q_out, k, v)
+
+    before = k.clone(), v.clone()
+    for shape in ((pages, page, hkv, d), (pages * page, hkv, d), (2 * pages, hkv, page // 2, d), (pages // 2, hkv, 2 * page, d),
+                  (hkv, pages, page, d), (pages, hkv, d, page), (pages, hkv, page // 3 + 1, d)):
+        other = torch.zeros(shape, dtype=BF16, device="cuda")
+        for kw in (dict(k=other), dict(v=other)):
+            with pytest.raises(ValueError, match="pool"):
+                decode(**kw)
+            with pytest.raises(ValueError, match="pool"):
+                write(**kw)
+    with pytest.raises(ValueError, match="out"):
+        decode(out=torch.zeros(hq, n, d, dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError, match="lse"):
+        decode(lse=torch.zeros(hq, n, device="cuda"))
+    with pytest.raises(ValueError, match="q_out"):
+        write(q_out=torch.zeros(hq, n, d, dtype=BF16, device="cuda"))
+    assert torch.equal(k, before[0]) and torch.equal(v, before[1])
+    want = decode()
+    for shape in ((pages, hkv, page * d), (pages * hkv, page, d), (pages * hkv * page * d,), (1, pages, 1, hkv, page, 1, d)):
+        assert torch.equal(decode(k.view(shape), v.view(shape)), want)
+    assert torch.equal(decode(out=torch.zeros(n, hq * d, dtype=BF16, device="cuda")).view(n, hq, d), want)
+    flat = torch.zeros(n * hq, device="cuda")
+    assert torch.equal(decode(lse=flat), want) and flat.all()
+    write(k.view(-1), v.view(pages, hkv, -1), q_out=torch.empty(n, hq * d, dtype=BF16, device="cuda"))
+    assert torch.equal(k[0, :, 3], kv[0]) and torch.equal(v[3, :, 2], kv[1])

@@ -49,6 +49,8 @@ std::string shown(const at::Tensor &t) {
     return s + " on " + t.device().str();
 }
 
+at::ScalarType type_of(const zha_paged_config *c) { return c->dtype == ZHA_BF16 ? at::kBFloat16 : at::kFloat; }
+
 // One call's arguments: its name for messages, and the device that all its tensors must be on.
 struct Call {
     const char *where;
@@ -78,16 +80,34 @@ struct Call {
         stride = n > 1 ? t.stride(0) : heads * d;
         return t.data_ptr();
     }
-    // contiguous, of at least (or exactly) n elements
-    void *block(PyObject *o, const char *name, int64_t n, at::ScalarType type, bool exact) const {
+    // contiguous, of at least n elements; None passes
+    int32_t *ints(PyObject *o, const char *name, int64_t n) const {
+        if (o == Py_None) return nullptr;
         const at::Tensor &t = tensor(o, name);
-        if (t.scalar_type() != type || t.get_device() != dev || !t.is_contiguous() || (exact ? t.numel() != n : t.numel() < n))
-            refuse(name, std::string("a contiguous ") + c10::toString(type) + " tensor of " + (exact ? "" : "at least ") +
-                             std::to_string(n) + " elements on device " + std::to_string(dev), t);
+        if (t.scalar_type() != at::kInt || t.get_device() != dev || !t.is_contiguous() || t.numel() < n)
+            refuse(name, "a contiguous Int tensor of at least " + std::to_string(n) + " elements on device " + std::to_string(dev), t);
+        return static_cast<int32_t *>(t.data_ptr());
+    }
+    // contiguous, of these dimensions. Neighbouring ones may be one, or split by ones: what leaves the elements in their
+    // order (every dimension's stride is one of the array's); other shapes of as many elements are another layout.
+    void *array(PyObject *o, const char *name, at::IntArrayRef dims, at::ScalarType type) const {
+        const at::Tensor &t = tensor(o, name);
+        int64_t total = 1, at = 1;
+        for (int64_t d : dims) total *= d;
+        bool same = t.numel() == total && t.is_contiguous();
+        size_t left = dims.size();
+        int64_t stride = 1;                // of dimension `left`, as if it were one of the array's
+        for (int64_t i = t.dim() - 1; i >= 0 && same && total > 0; --i) {
+            at *= t.size(i);
+            while (stride < at && left > 0) stride *= dims[--left];
+            same = stride == at;
+        }
+        if (!same || t.scalar_type() != type || t.get_device() != dev)
+            refuse(name, std::string("a contiguous ") + c10::toString(type) + " " + list(dims) + " on device " + std::to_string(dev), t);
         return t.data_ptr();
     }
-    int32_t *ints(PyObject *o, const char *name, int64_t n) const {      // None passes
-        return o == Py_None ? nullptr : static_cast<int32_t *>(block(o, name, n, at::kInt, false));
+    void *pool(PyObject *o, const char *name, const zha_paged_config *c) const {
+        return array(o, name, {c->n_pages, c->n_kv_heads, c->page_size, c->head_dim}, type_of(c));
     }
     // [batch, max_pages], or flat: a table of another width would be read askew
     int32_t *table(PyObject *o, const zha_paged_config *cfg) const {
@@ -109,10 +129,6 @@ struct Call {
     }
 };
 
-at::ScalarType type_of(const zha_paged_config *c) { return c->dtype == ZHA_BF16 ? at::kBFloat16 : at::kFloat; }
-int64_t pool_elements(const zha_paged_config *c) {
-    return (int64_t)c->n_pages * c->n_kv_heads * c->page_size * c->head_dim;
-}
 
 // The memory of a ctypes structure (which its owner keeps). Only of the right type: any other one would be read askew.
 template <typename S>
@@ -247,7 +263,7 @@ PyObject *paged_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (a[1] != Py_None) is_rotary(a[1]);
         c.on(c.tensor(a[8], "k_pool"));
         const auto type = type_of(cfg);
-        const int64_t d = cfg->head_dim, hkv = cfg->n_kv_heads, hq = cfg->n_q_heads, size = pool_elements(cfg);
+        const int64_t d = cfg->head_dim, hkv = cfg->n_kv_heads, hq = cfg->n_q_heads;
         const at::Tensor &k = c.tensor(a[3], "k_new");
         const int64_t tokens = k.dim() ? k.size(0) : 0;
         if (tokens > INT32_MAX) c.refuse("too many tokens");
@@ -257,10 +273,10 @@ PyObject *paged_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (a[2] != Py_None) {
             qp = c.rows(a[2], "q", tokens, hq, d, type, qs);
             if (a[7] == Py_None) c.refuse("q_out is needed with q");
-            qo = c.block(a[7], "q_out", tokens * hq * d, type, true);
+            qo = c.array(a[7], "q_out", {tokens, hq, d}, type);
         }
         const int32_t *pos = c.ints(a[5], "positions", tokens), *slots = c.ints(a[6], "slots", tokens);
-        void *k_pool = c.block(a[8], "k_pool", size, type, true), *v_pool = c.block(a[9], "v_pool", size, type, true);
+        void *k_pool = c.pool(a[8], "k_pool", cfg), *v_pool = c.pool(a[9], "v_pool", cfg);
         int32_t *status = c.ints(a[10], "dev_status", 1);
         const zha_rotary *r = rotation(c, a[1]);
         if (a[12] == Py_True)
@@ -279,18 +295,18 @@ PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &q = c.tensor(a[1], "q");
         c.on(q);
         const auto type = type_of(cfg);
-        const int64_t d = cfg->head_dim, hq = cfg->n_q_heads, B = cfg->batch, size = pool_elements(cfg);
+        const int64_t d = cfg->head_dim, hq = cfg->n_q_heads, B = cfg->batch;
         const int64_t rows = q.dim() == 3 ? q.size(0) : -1;
         if (rows < 0 || rows > INT32_MAX || q.size(1) != hq || q.size(2) != d)
             c.refuse("q", "[n, " + std::to_string(hq) + ", " + std::to_string(d) + "]", q);
         if (a[9] == Py_None && rows > B) c.refuse("q", "of no more rows than sequences where seq_ids is not given", q);
-        void *qp = c.block(a[1], "q", rows * hq * d, type, true), *out = c.block(a[6], "out", rows * hq * d, type, true);
-        float *lse = a[8] == Py_None ? nullptr : static_cast<float *>(c.block(a[8], "lse", rows * hq, at::kFloat, true));
+        void *qp = c.array(a[1], "q", {rows, hq, d}, type), *out = c.array(a[6], "out", {rows, hq, d}, type);
+        float *lse = a[8] == Py_None ? nullptr : static_cast<float *>(c.array(a[8], "lse", {rows, hq}, at::kFloat));
         const at::Tensor &ws = c.tensor(a[7], "workspace");
         const size_t need = rows ? f_workspace(cfg, (int32_t)rows) : 0;
         if (ws.get_device() != c.dev || !ws.is_contiguous() || ws.nbytes() < need)
             c.refuse("workspace", "contiguous, on the call's device and of at least " + std::to_string(need) + " bytes", ws);
-        const void *k_pool = c.block(a[2], "k_pool", size, type, true), *v_pool = c.block(a[3], "v_pool", size, type, true);
+        const void *k_pool = c.pool(a[2], "k_pool", cfg), *v_pool = c.pool(a[3], "v_pool", cfg);
         const int32_t *table = c.table(a[4], cfg), *lens = c.ints(a[5], "lens", B);
         const int32_t *seq = c.ints(a[9], "seq_ids", rows), *pos = c.ints(a[10], "positions", rows);
         int32_t *status = c.ints(a[11], "dev_status", 1);
