@@ -1046,10 +1046,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 ++round;
             }
         }
-        // given up: the copies in flight still land before the CTA may end
-        if (k < n)
-            for (int j = k < S::kStages ? 0 : k - S::kStages; j < k; ++j)
-                mbar_wait_bounded(smem_u32(&sm.full[j % S::kStages]), (j / S::kStages) & 1, kWaitCycles, nullptr, a.status);
+        // The copies in flight land before the CTA may end, also where another warp has given up on one (it does not
+        // wait for those behind it).
+        for (int j = k < S::kStages ? 0 : k - S::kStages; j < k; ++j)
+            mbar_wait_bounded(smem_u32(&sm.full[j % S::kStages]), (j / S::kStages) & 1, kWaitCycles, nullptr, a.status);
         return;
     }
 
