@@ -1,5 +1,8 @@
 """PagedCache and the binding's argument handling without a GPU (nothing here launches): a refused call changes nothing."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -138,3 +141,63 @@ def test_structures_of_another_type_are_refused(zha):
                 call(cfg, bad, q, kv, kv, i32, i32, q, pool, pool)
     with pytest.raises(TypeError, match="Rotary"):
         zha.rotary(None, q, kv, i32)
+
+
+# ---------------------------------------------------------------- the binding's module and what it was built for
+
+def test_the_module_is_rebuilt_for_another_torch_or_python(monkeypatch, tmp_path):
+    """As file times alone would not: it is compiled against one torch's C++ headers and one Python's."""
+    import sysconfig
+
+    from tree_indexed_sparse_02_b200 import build
+    made = []
+
+    def compiler(cmd):
+        made.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("module")
+
+    monkeypatch.setattr(build.subprocess, "check_call", compiler)
+    monkeypatch.setattr(build, "BIND", str(tmp_path / "_bind.so"))
+    monkeypatch.setattr(build, "BIND_KEY", str(tmp_path / "at" / "_bind.key"), raising=False)
+    config_var = sysconfig.get_config_var
+
+    def builds():
+        n = len(made)
+        assert build.build_bind() == build.BIND and os.path.exists(build.BIND)
+        return len(made) - n
+
+    assert [builds(), builds()] == [1, 0]
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".1")
+    assert [builds(), builds()] == [1, 0]
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda x: ".other.so" if x == "EXT_SUFFIX" else config_var(x))
+    assert [builds(), builds()] == [1, 0]
+    os.remove(build.BIND)
+    assert [builds(), builds()] == [1, 0]
+    os.utime(build.BIND, (1, 1))                             # older than its source
+    assert builds() == 1
+    n = len(made)
+    build.build_bind(force=True)
+    assert len(made) == n + 1
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def python(code):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+
+
+def test_a_module_of_another_torch_is_not_used(zha):
+    """It would load, and read tensors of another layout."""
+    r = python("""
+import torch
+torch.__version__ = "1.0.another"
+try:
+    from tree_indexed_sparse_02_b200 import zha
+    zha.rotary(zha.Rotary(64, device="cpu"), torch.zeros(1, 1, 64), None, torch.zeros(1, dtype=torch.int32))
+except ImportError as e:
+    assert "1.0.another" in str(e) and "build.py" in str(e), e
+    print("refused")
+""")
+    assert r.stdout.strip() == "refused", r.stdout + r.stderr

@@ -15,6 +15,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libzha.so")
 BIND_SRC = os.path.join(CSRC, "zha_bind.cpp")
 BIND = os.path.join(HERE, "_bind.so")
+BIND_KEY = os.path.join(HERE, "_build", "_bind.key")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++20",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -44,16 +45,33 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def build_bind(force: bool = False, verbose: bool = False) -> str:
+def bind_key() -> str:
+    """What _bind.so is built for: its tensors and objects are those of one torch and one Python."""
+    import torch
+    return "torch %s, C++11 ABI %d, Python %s" % (torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                                                  sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def _bind_stale() -> bool:
+    if not os.path.exists(BIND) or not os.path.exists(BIND_KEY):
+        return True
+    with open(BIND_KEY) as f:
+        if f.read() != bind_key():
+            return True
     newest = max(os.path.getmtime(p) for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) > newest:
+    return os.path.getmtime(BIND) <= newest
+
+
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    if not force and not _bind_stale():
         return BIND
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = BIND + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE]
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DZHA_BIND_KEY="%s"' % bind_key(), "-I", INCLUDE]
     for inc in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
         cmd += ["-isystem", inc]
@@ -63,6 +81,9 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, BIND)
+    os.makedirs(os.path.dirname(BIND_KEY), exist_ok=True)
+    with open(BIND_KEY, "w") as f:
+        f.write(bind_key())
     return BIND
 
 

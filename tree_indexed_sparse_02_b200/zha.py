@@ -14,10 +14,15 @@ import os
 
 import torch
 
+from .build import bind_key
+
 try:
     from . import _bind
 except ImportError as e:
     raise ImportError(f"_bind.so not built or not loadable ({e}); run tree_indexed_sparse_02_b200/build.py") from e
+if getattr(_bind, "built_for", None) != bind_key():
+    raise ImportError(f"_bind.so was built for {getattr(_bind, 'built_for', 'another version')}, this is {bind_key()}; "
+                      "run tree_indexed_sparse_02_b200/build.py")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzha.so")
