@@ -201,3 +201,22 @@ except ImportError as e:
     print("refused")
 """)
     assert r.stdout.strip() == "refused", r.stdout + r.stderr
+
+
+def test_the_sparse_path_does_not_need_the_module(zha):
+    r = python("""
+import sys
+sys.modules["tree_indexed_sparse_02_b200._bind"] = None
+import torch
+from tree_indexed_sparse_02_b200 import zha
+assert zha.workspace_bytes(zha.config(2, 8, 2, 64, 16, 2, 1)) > 0
+cfg, rot, x, i = zha.paged_config(1, 1, 1, 64, 16, 1, 1), zha.Rotary(64, device="cpu"), torch.zeros(1, 1, 64), torch.zeros(9, dtype=torch.int32)
+m = {"positions": i, "slots": i, "seq_ids": i, "cu": i}
+for call in (lambda: zha.rotary(rot, x, None, i), lambda: zha.paged_plan(cfg, i, i, i, i, i, m),
+             lambda: zha.paged_write(cfg, rot, x, x, x, i, i, x, x, x), lambda: zha.paged_decode(cfg, x, x, x, i, i, x, i)):
+    try:
+        call()
+    except ImportError as e:
+        print("build.py" in str(e))
+""")
+    assert r.stdout.split() == ["True"] * 4, r.stdout + r.stderr

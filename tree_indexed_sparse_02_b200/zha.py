@@ -3,8 +3,8 @@
 Argument marshalling only: every function forwards device pointers of torch
 tensors and a CUDA stream to the library, and raises ``ZhaError`` on a
 non-zero status. Nothing here computes any step of the method; if libzha.so
-(or _bind.so, the marshalling of the paged and rotary calls) is missing the
-import fails loudly (there is no fallback path).
+is missing the import fails loudly, and without _bind.so, the marshalling of
+the paged and rotary calls, those calls do (there is no fallback path).
 """
 from __future__ import annotations
 
@@ -15,14 +15,6 @@ import os
 import torch
 
 from .build import bind_key
-
-try:
-    from . import _bind
-except ImportError as e:
-    raise ImportError(f"_bind.so not built or not loadable ({e}); run tree_indexed_sparse_02_b200/build.py") from e
-if getattr(_bind, "built_for", None) != bind_key():
-    raise ImportError(f"_bind.so was built for {getattr(_bind, 'built_for', 'another version')}, this is {bind_key()}; "
-                      "run tree_indexed_sparse_02_b200/build.py")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzha.so")
@@ -336,9 +328,30 @@ class Rotary:
 # The calls below check their arguments (tensors' type, shape, layout, device: ValueError; PagedConfig and Rotary:
 # TypeError) and pass them on in csrc/zha_bind.cpp: on the GPU they can take less time than Python takes to look at
 # the tensors' attributes.
-_bind.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
-             for name in ("zha_rotary_apply", "zha_paged_plan", "zha_paged_write", "zha_paged_decode",
-                          "zha_paged_workspace_bytes", "zha_paged_write_check")), PagedConfig, Rotary)
+# Where that module cannot be loaded, they raise; the calls of the sparse path need ctypes alone.
+
+class _NoBind:
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_bind.so {self._why}; run tree_indexed_sparse_02_b200/build.py")
+
+
+def _load_bind():
+    try:
+        from . import _bind
+    except ImportError as e:
+        return _NoBind(f"not built or not loadable ({e})")
+    if getattr(_bind, "built_for", None) != bind_key():
+        return _NoBind(f"was built for {getattr(_bind, 'built_for', 'another version')}, this is {bind_key()}")
+    _bind.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
+                 for name in ("zha_rotary_apply", "zha_paged_plan", "zha_paged_write", "zha_paged_decode",
+                              "zha_paged_workspace_bytes", "zha_paged_write_check")), PagedConfig, Rotary)
+    return _bind
+
+
+_bind = _load_bind()
 
 
 def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
