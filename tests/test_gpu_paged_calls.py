@@ -178,3 +178,33 @@ def test_arrays_of_another_layout_are_refused(zha):
     assert torch.equal(decode(lse=flat), want) and flat.all()
     write(k.view(-1), v.view(pages, hkv, -1), q_out=torch.empty(n, hq * d, dtype=BF16, device="cuda"))
     assert torch.equal(k[0, :, 3], kv[0]) and torch.equal(v[3, :, 2], kv[1])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (16, 1), (6, 2)])
+def test_a_token_with_all_the_weight_comes_out_exactly(zha, dt, d, hq, hkv):
+    """Its weight is 2^0 = 1; every other score is more than 150 / ln 2 below, so that its weight is 0 in fp32. The sum
+    of the weights is 1 and the output is the token's value row, bit for bit, in rows of one CTA and in split ones."""
+    lens, at = [200, 9000, 1, 9000], [85, 8999, 0, 3]
+    pages = sum(-(-n // 16) for n in lens)
+    width = -(-max(lens) // 16)
+    cfg = zha.paged_config(4, hq, hkv, d, 16, pages, width, dtype="bf16" if dt is BF16 else "f32")
+    g = torch.Generator().manual_seed(d + hq)
+    k, v = (torch.randn(pages, hkv, 16, d, generator=g).to(dt).cuda() for _ in range(2))
+    table, first = torch.full((4, width), -1, dtype=torch.int32), 0
+    for b, n in enumerate(lens):
+        count = -(-n // 16)
+        table[b, :count] = torch.arange(first, first + count)
+        first += count
+    table = table.cuda()
+    q = (torch.rand(4, hq, d, generator=g) + 0.1).to(dt).cuda()
+    want = torch.empty_like(q)
+    for b, t in enumerate(at):
+        k[table[b, t // 16], :, t % 16] = 3e4                # a score of 3e4 sum(q) / sqrt(d) > 20,000; the others' are below 200
+        want[b] = v[table[b, t // 16], :, t % 16].repeat_interleave(hq // hkv, dim=0)
+    out, status = torch.zeros_like(q), ints([0])
+    zha.paged_decode(cfg, q, k, v, table, ints(lens), out, zha.paged_workspace(cfg, 4), dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert torch.equal(out, want)
