@@ -491,8 +491,8 @@ ZHA_API zha_status zha_rotary_freqs(int32_t rotary_dim, double base, int32_t sca
  * (same pointer and stride); other overlaps are not supported. Either of q and
  * k may be absent (null, with its output). transpose != 0 applies the
  * transposed map, which is the gradient of the rotation (and, for mscale 1,
- * its inverse). Sines and cosines come from fp64 angles, products are fp32,
- * each output is rounded once. dtype ZHA_BF16 or ZHA_F32, head_dim 64 or 128,
+ * its inverse). Angles are formed and reduced in fp64; their sines and cosines,
+ * mscale and the products are fp32, each output is rounded once. dtype ZHA_BF16 or ZHA_F32, head_dim 64 or 128,
  * at most 1,024 heads each and 2^30 tokens, strides below 2^30 elements.
  */
 ZHA_API zha_status zha_rotary_apply(const zha_rotary *rotary, int32_t head_dim, int32_t dtype,
@@ -551,8 +551,10 @@ ZHA_API size_t zha_paged_workspace_bytes(const zha_paged_config *cfg, int32_t n_
  * position outside [0, lens) ZHA_ERR_INVALID_ARG: the row gets zeros and -inf
  * (beyond the batch: is left). A page number outside the pool sets
  * ZHA_ERR_INVALID_ARG and its tokens are skipped. Cache rows outside the
- * attended range are not read into any result, whatever they hold. Softmax
- * statistics and sums are fp32. The result does not depend on timing (a split
+ * attended range are not read into any result, whatever they hold. Scores,
+ * softmax statistics and sums are fp32; a bf16 cache's weights multiply its
+ * values as two bf16 parts (16 bits together, summed in fp32), an fp32 one's as
+ * they are. The result does not depend on timing (a split
  * row's parts are joined in a fixed order). A row whose every score is -inf
  * gets zeros and -inf as well. Every wait inside is bounded (about two
  * seconds): ZHA_ERR_TIMEOUT, the results are then invalid and the workspace is

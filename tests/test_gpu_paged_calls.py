@@ -208,3 +208,25 @@ def test_a_token_with_all_the_weight_comes_out_exactly(zha, dt, d, hq, hkv):
     torch.cuda.synchronize()
     assert int(status) == 0
     assert torch.equal(out, want)
+
+
+def test_a_table_of_the_users_own(zha):
+    """Frequencies and factor put into a Rotary in place are what the next calls use. fp32, in units of 2^-24 of the
+    pair's size: sine, cosine, the factor and its product 8, two products and a sum 3; the angle 2^-51 of itself."""
+    import numpy as np
+
+    import paged_testlib as P
+    rot = zha.Rotary(64)
+    theta = np.linspace(0.9, 0.001, 32) ** 2
+    rot.freq.copy_(torch.from_numpy(theta / (2 * np.pi)))
+    rot.desc.mscale = 1.25
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(7, 3, 64, generator=g).cuda()
+    pos = torch.randint(0, 9000, (7,), generator=g, dtype=torch.int32)
+    y = torch.empty_like(x)
+    zha.rotary(rot, x, None, pos.cuda(), y)
+    xs = P.np64(x)
+    want = P.rotate(xs, pos.numpy(), 64, "half", theta, 1.25)
+    far = np.tile(pos.numpy()[:, None] * theta[None, :] * 2.0 ** -51, 2)[:, None, :]
+    tol = 2.0 ** -24 * np.abs(want) + 1.25 * P.pair_size(xs, 64, "half") * (11 * 2.0 ** -24 + far)
+    assert np.all(np.abs(P.np64(y) - want) <= tol)

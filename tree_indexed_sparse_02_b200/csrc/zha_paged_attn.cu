@@ -9,11 +9,12 @@
 //
 // Bound: one read of the attended K and V rows from HBM (8 flops a byte at 8
 // query heads per KV head, far below the tensor cores' rate). B200, launches in
-// a graph: 4 rows of 262,144 tokens, 32/4 heads, d 128, bf16 332 us (2.15 GB:
-// 6.47 TB/s, 99% of the measured copy); 64 rows of 16 to 16,384 tokens 79 us
-// (83%); one row of 200 tokens 7.9 us (latency: code and translations are cold
-// in every launch); fp32, 6 rows of 60,001 tokens, 16/2 heads, d 64, 82 us (69%,
-// bound by its instructions).
+// a graph: 4 rows of 262,144 tokens, 32/4 heads, d 128, bf16 334 us (2.15 GB:
+// 6.43 TB/s, 98% of the measured copy; 315 to 343 us from card to card); 64 rows
+// of 16 to 16,384 tokens 77 us (85%); one row of 200 tokens 8.2 us (latency: code
+// and translations are cold in every launch); fp32, 6 rows of 60,001 tokens,
+// 16/2 heads, d 64, 83 us (68%, bound by its instructions). Rows of one sequence
+// share nothing: a prompt's rows each read their prefix (4,096 tokens 2.6 ms).
 //
 // Work: the K/V rows of a (row, KV head) -- a group -- are cut into tiles of
 // 16 KB of K and 16 KB of V; all groups' tiles form one list, and every CTA
@@ -161,8 +162,8 @@ struct Shared {
     // K then V of a tile: blocks of 8 tokens, [ROWB / 128][8][128 bytes], 16-byte chunks XOR-swizzled by the row
     // (the 128-byte swizzle of a TMA copy)
     uint8_t ring[kStages][2 * kTileBytes];
-    // The weights. bf16: as MMA operand rows [head][token], in two parts (16 bits; one bf16 part alone would cost
-    // half an ulp of the output), padded against bank conflicts; fp32: [token][head].
+    // The weights. bf16: as MMA operand rows [head][token], in two parts (16 bits, which moves about one output in a
+    // thousand by a bf16 step; one bf16 part alone would cost half an ulp of the output), padded against bank conflicts; fp32: [token][head].
     typedef typename std::conditional<kBf16, __nv_bfloat16[2][kRows][TT + 8], float[TT][kRows]>::type Weights;
     alignas(16) Weights p;
     alignas(16) float score[!kBf16 && D == 128 && GP == 16 ? TT : 1][kRows];     // between a tile's scores and its weights

@@ -299,7 +299,8 @@ class Rotary:
     """A rotary embedding: its frequency table (turns per position, fp64) on the device.
 
     layout "half" pairs coordinates (i, i + rotary_dim/2), "interleaved" (2i, 2i + 1); scaling "none",
-    "linear", "ntk" or "yarn" by `factor` (from a context of original_len for YaRN)."""
+    "linear", "ntk" or "yarn" by `factor` (from a context of original_len for YaRN). Another table is put into `freq`
+    in place (rotary_dim / 2 turns per position; desc.mscale for another factor of the values)."""
 
     def __init__(self, rotary_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_len=4096,
                  device="cuda"):
@@ -356,7 +357,8 @@ _bind = _load_bind()
 
 def rotary(rot: Rotary, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
     """Rotate q [n, Hq, d] and k [n, Hk, d] (either may be None; tokens may be strided) at int32 positions [n].
-    The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out)."""
+    The outputs default to the inputs (in place); transpose applies the gradient's map. Returns (q_out, k_out).
+    Nothing is recorded for autograd (as in every call here): a backward pass calls this with transpose."""
     code = _bind.rotary(rot, q, k, positions, q_out, k_out, transpose,
                         None if stream is None else stream.cuda_stream)
     if code:
@@ -457,7 +459,10 @@ class PagedCache:
     def step(self, n_new, q, k_new, v_new, stream=None):
         """q [max_tokens, Hq, d], k_new, v_new [max_tokens, Hkv, d]: the step's token rows, before rotation.
 
-        A step whose arguments are refused changes nothing: they are checked before the plan moves lengths and pages."""
+        Returns the cache's own out [max_tokens, Hq, d] and lse [max_tokens, Hq]. Rows that belong to no token, or to a
+        sequence that was not served (pages or table full: check_status raises ZHA_ERR_CAPACITY), keep what an
+        earlier step left in them. A step whose arguments are refused changes nothing: they are checked before the
+        plan moves lengths and pages."""
         if q is None:
             raise ValueError("PagedCache.step: q must be a tensor (write() puts keys and values alone)")
         m = self.token_map
@@ -542,8 +547,8 @@ class DecodeGraph:
 
     def stage(self, q, k_new, v_new):
         """Put a step's inputs into the graph's own buffers (one multi-tensor
-        copy, or the rotation and a copy of v_new); a caller that produces them
-        there directly skips this."""
+        copy, or the rotation, of q and k_new on the device, and a copy of v_new);
+        a caller that produces them there directly skips this."""
         if self.rot is not None:
             rotary(self.rot, q, k_new, self.lens, self.q, self.k_new)
             self.v_new.copy_(v_new, non_blocking=True)
